@@ -303,6 +303,76 @@ W8A8_API int w8a8_gemm_rmsnorm_quant_ex(const int8_t *xq, const float *s_tok, co
                                         w8a8_stream_t stream);
 
 /*
+ * ---------------------------------------------------------------- norms at a block boundary
+ *
+ * The row operators between two blocks whose output is normalized, gated and added to a scaled
+ * residual stream before the next block's smoothed RMSNorm and quantization, in one pass
+ * [W8A8 "How SmoothQuant prevents outliers in activation tensors" (the RMSNorm with gamma / s);
+ * the norm after the block, the gate and the residual scale are not on the pages]:
+ *   n[m,j]  = (float(y[m,j]) * r1[m]) * gamma_post[j]       (gamma_post NULL: n = float(y))
+ *   b[m,j]  = gate * n[m,j]                                 (no gate: b = n)
+ *   h[m,j]  = bf16(res_scale * float(residual[m,j]) + b[m,j])
+ *   z[m,j]  = (h[m,j] * r2[m]) * gamma_smoothed[j]
+ *   s_tok, q from z exactly as in w8a8_quantize_rows (_fp8: w8a8_quantize_rows_fp8)
+ * with r1 = 1 / sqrt(mean(y^2) + eps_post), r2 = 1 / sqrt(mean(h^2) + eps), the means in binary64
+ * rounded once as in w8a8_smooth_rmsnorm_quant, and every product and sum its own binary32
+ * operation. gate_kind says what `gate` is: W8A8_GATE_NONE (gate NULL), W8A8_GATE_TOKEN (fp32
+ * [M], one factor per token), W8A8_GATE_CHANNEL (fp32 [K]), W8A8_GATE_FULL (bf16 [M,K]).
+ * y, residual, h_out: bf16 [M,K]; gamma_post, gamma_smoothed: fp32 [K]; q [M,K]; s_tok fp32 [M];
+ * all but s_tok and a per-token gate 16-byte aligned. h_out may be residual (in place), nothing
+ * else may alias an output. res_scale finite, eps >= 0, eps_post >= 0 (ignored without
+ * gamma_post). Shapes as for w8a8_smooth_rmsnorm_quant.
+ */
+enum w8a8_gate {
+    W8A8_GATE_NONE = 0,
+    W8A8_GATE_TOKEN = 1,
+    W8A8_GATE_CHANNEL = 2,
+    W8A8_GATE_FULL = 3
+};
+
+W8A8_API int w8a8_sandwich_rmsnorm_quant(const w8a8_bf16 *y, const w8a8_bf16 *residual,
+                                         const float *gamma_post, float eps_post,
+                                         const void *gate, int gate_kind, float res_scale,
+                                         const float *gamma_smoothed, float eps, int64_t M,
+                                         int64_t K, w8a8_bf16 *h_out, int8_t *q, float *s_tok,
+                                         w8a8_stream_t stream);
+W8A8_API int w8a8_sandwich_rmsnorm_quant_fp8(const w8a8_bf16 *y, const w8a8_bf16 *residual,
+                                             const float *gamma_post, float eps_post,
+                                             const void *gate, int gate_kind, float res_scale,
+                                             const float *gamma_smoothed, float eps, int64_t M,
+                                             int64_t K, w8a8_bf16 *h_out, uint8_t *q,
+                                             float *s_tok, w8a8_stream_t stream);
+
+/*
+ * The backward pass of the call above, for tuning the floating-point parts of a quantized model.
+ * The quantization is passed straight through (its scale is the row's own maximum, so nothing is
+ * clipped): dz is the gradient of the values the codes stand for, as w8a8_gemm_dgrad of the next
+ * linear gives it. dh: the gradient that reaches h by the residual stream, or NULL (zero). y, h:
+ * the forward call's input and its stored output. Per row, in binary32:
+ *   D            = dh + r2 (w - h r2^2 mean(w h)),  w = dz gamma_smoothed    (gradient of h)
+ *   dresidual    = bf16(res_scale D)
+ *   dy           = bf16(r1 (v - y r1^2 mean(v y))), v = gate gamma_post D    (gate D without it)
+ *   dgamma_smoothed[j] = sum_m dz h r2;  dgamma_post[j] = sum_m gate D y r1
+ *   dgate        = D n: summed over the channels (W8A8_GATE_TOKEN, fp32 [M]), over the tokens
+ *                  (W8A8_GATE_CHANNEL, fp32 [K]), or elementwise (W8A8_GATE_FULL, bf16 [M,K])
+ * The sums over tokens are taken per CTA and then added in a fixed order: the same call gives the
+ * same bits on the same device. dgamma_post is NULL exactly when gamma_post is, dgate exactly
+ * when gate is. dresidual may be dh (in place); no other output may alias an input or another
+ * output. Alignment as above (the fp32 gradients need none). workspace:
+ * w8a8_sandwich_rmsnorm_backward_workspace_size(M, K) bytes, 16-byte aligned, any contents.
+ */
+W8A8_API size_t w8a8_sandwich_rmsnorm_backward_workspace_size(int64_t M, int64_t K);
+W8A8_API int w8a8_sandwich_rmsnorm_backward(const w8a8_bf16 *dz, const w8a8_bf16 *dh,
+                                            const w8a8_bf16 *y, const w8a8_bf16 *h,
+                                            const float *gamma_post, float eps_post,
+                                            const void *gate, int gate_kind, float res_scale,
+                                            const float *gamma_smoothed, float eps, int64_t M,
+                                            int64_t K, w8a8_bf16 *dy, w8a8_bf16 *dresidual,
+                                            float *dgamma_post, void *dgate,
+                                            float *dgamma_smoothed, void *workspace,
+                                            size_t workspace_bytes, w8a8_stream_t stream);
+
+/*
  * ---------------------------------------------------------------- the fused decoder block
  *
  * One Llama decoder block's whole linear path at decode sizes (1 <= M <= 64 tokens) as a single

@@ -9,6 +9,7 @@ package does not need a GPU, but every compute call does.
     q, s = w8a8_smooth_rmsnorm_quant(x, gamma_smoothed, eps)
     y = w8a8_gemm_dequant(q, s, wq, s_ch)
 """
+import contextlib
 import ctypes as C
 import os
 import threading
@@ -30,6 +31,8 @@ __all__ = [
     "w8a8_gemm_silu_quant_fp8_workspace_size",
     "w8a8_gptq_quantize", "w8a8_gptq_workspace_size", "w8a8_probe_f64_fma",
     "w8a8_block_decode", "w8a8_block_decode_workspace_size", "BlockBuffers",
+    "w8a8_sandwich_rmsnorm_quant", "w8a8_sandwich_rmsnorm_quant_fp8",
+    "w8a8_sandwich_rmsnorm_backward", "w8a8_sandwich_rmsnorm_backward_workspace_size",
     "Workspace", "FP8",
 ]
 
@@ -80,6 +83,13 @@ SIGNATURES = [
     ("w8a8_gptq_workspace_size", _SZ, [_I64, _I64]),
     ("w8a8_block_decode_workspace_size", _SZ, [_I64, _I64, _I64, _I64]),
     ("w8a8_block_decode", _I, [_P, _P, _SZ, _P]),
+    ("w8a8_sandwich_rmsnorm_quant", _I, [_P, _P, _P, _F, _P, _I, _F, _P, _F, _I64, _I64, _P, _P,
+                                         _P, _P]),
+    ("w8a8_sandwich_rmsnorm_quant_fp8", _I, [_P, _P, _P, _F, _P, _I, _F, _P, _F, _I64, _I64, _P,
+                                             _P, _P, _P]),
+    ("w8a8_sandwich_rmsnorm_backward_workspace_size", _SZ, [_I64, _I64]),
+    ("w8a8_sandwich_rmsnorm_backward", _I, [_P, _P, _P, _P, _P, _F, _P, _I, _F, _P, _F, _I64,
+                                            _I64, _P, _P, _P, _P, _P, _P, _SZ, _P]),
     ("w8a8_probe_f64_fma", _I, [C.c_longlong, _I, _P, _P]),
     ("w8a8_gptq_quantize", _I, [_P, _P, _P, _I64, _I64, _I64, C.c_double, _P, _P, _P, _P, _SZ,
                                 _P]),
@@ -144,6 +154,45 @@ def _need(t, name, dtype, shape=None):
         raise ValueError(f"{name} must be contiguous")
     if shape is not None and tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+
+
+_HERE = contextlib.nullcontext()
+
+
+def _place(x, stream):
+    """The context a call runs in: x's device current, and the given stream (default: the current
+    stream of x's device), so that outputs and workspaces allocated inside belong to the stream
+    that uses them."""
+    if stream is None:
+        if x.device.index == torch.cuda.current_device():
+            return _HERE
+        stream = torch.cuda.current_stream(x.device)
+    elif stream.device != x.device:
+        raise ValueError(f"stream is on {stream.device}, the tensors on {x.device}")
+    return torch.cuda.stream(stream)
+
+
+def _same_device(x, **tensors):
+    for name, t in tensors.items():
+        if t is not None and t.device != x.device:
+            raise ValueError(f"{name} is on {t.device}, expected {x.device}")
+
+
+def _scratch(workspace, nbytes, device):
+    """(pointer, size) of the caller's workspace, or of a new one for this call alone (nothing is
+    kept between calls that use it, so calls on any streams and captured graphs cannot share it).
+    The last element keeps it alive."""
+    if workspace is None:
+        workspace = torch.empty(nbytes, dtype=torch.uint8, device=device) if nbytes else None
+    elif isinstance(workspace, Workspace):
+        workspace, _ = workspace.get(nbytes)
+    else:
+        _need(workspace, "workspace", workspace.dtype)
+        if workspace.device != device:
+            raise ValueError(f"workspace is on {workspace.device}, expected {device}")
+    if workspace is None:
+        return None, 0, None
+    return _ptr(workspace), workspace.numel() * workspace.element_size(), workspace
 
 
 def w8a8_status_string(status: int) -> str:
@@ -685,3 +734,115 @@ def w8a8_block_decode(x, attn, gamma1, sinv_o, gamma2, qkv, o, gate_up_il, down,
     _check("w8a8_block_decode", lib().w8a8_block_decode(
         C.byref(io), _ptr(b.workspace), b.workspace.numel(), _stream(stream)))
     return b
+
+
+# kinds of gate of the block-boundary norms (enum w8a8_gate)
+_GATE_NONE, _GATE_TOKEN, _GATE_CHANNEL, _GATE_FULL = 0, 1, 2, 3
+
+
+def _gate_kind(gate, M, K):
+    if gate is None:
+        return _GATE_NONE
+    if not isinstance(gate, torch.Tensor):
+        raise TypeError("gate must be a torch.Tensor")
+    shape = tuple(gate.shape)
+    for kind, dtype, want in ((_GATE_TOKEN, torch.float32, (M, 1)),
+                              (_GATE_CHANNEL, torch.float32, (1, K)),
+                              (_GATE_FULL, torch.bfloat16, (M, K))):
+        if shape == want and gate.dtype == dtype:
+            _need(gate, "gate", dtype)
+            return kind
+    raise ValueError(f"gate must be fp32 ({M}, 1), fp32 (1, {K}) or bf16 ({M}, {K}), got "
+                     f"{gate.dtype} {shape}")
+
+
+def _sandwich_quant(name, code, y, residual, gamma_smoothed, eps, gamma_post, eps_post, gate,
+                    res_scale, h_out, q, s_tok, stream):
+    _need(y, "y", torch.bfloat16)
+    if y.dim() != 2:
+        raise ValueError(f"y must be [M, K], got {tuple(y.shape)}")
+    M, K = y.shape
+    _need(residual, "residual", torch.bfloat16, (M, K))
+    _need(gamma_smoothed, "gamma_smoothed", torch.float32, (K,))
+    if gamma_post is not None:
+        _need(gamma_post, "gamma_post", torch.float32, (K,))
+    kind = _gate_kind(gate, M, K)
+    with _place(y, stream):
+        h_out = torch.empty_like(y) if h_out is None else h_out
+        q = torch.empty((M, K), dtype=code, device=y.device) if q is None else q
+        s_tok = torch.empty(M, dtype=torch.float32, device=y.device) if s_tok is None else s_tok
+        _need(h_out, "h_out", torch.bfloat16, (M, K))
+        _need(q, "q", code, (M, K))
+        _need(s_tok, "s_tok", torch.float32, (M,))
+        _same_device(y, residual=residual, gamma_smoothed=gamma_smoothed, gamma_post=gamma_post,
+                     gate=gate, h_out=h_out, q=q, s_tok=s_tok)
+        _check(name, getattr(lib(), name)(
+            _ptr(y), _ptr(residual), _ptr(gamma_post), float(eps if eps_post is None else eps_post),
+            _ptr(gate), kind, float(res_scale), _ptr(gamma_smoothed), float(eps), M, K,
+            _ptr(h_out), _ptr(q), _ptr(s_tok), _stream(None)))
+    return q, s_tok, h_out
+
+
+def w8a8_sandwich_rmsnorm_quant(y, residual, gamma_smoothed, eps, gamma_post=None, eps_post=None,
+                                gate=None, res_scale=1.0, h_out=None, q=None, s_tok=None,
+                                stream=None):
+    """The step between two blocks: h = bf16(res_scale * residual + gate * n), with n the RMSNorm
+    of the block's output y by gamma_post (n = y without gamma_post), then the next block's
+    smoothed RMSNorm of h with per-token int8 codes. gate: None, fp32 [M, 1] (per token), fp32
+    [1, K] (per channel) or bf16 [M, K]. eps_post defaults to eps. h_out may be residual (in
+    place). Returns (q, s_tok, h)."""
+    return _sandwich_quant("w8a8_sandwich_rmsnorm_quant", torch.int8, y, residual, gamma_smoothed,
+                           eps, gamma_post, eps_post, gate, res_scale, h_out, q, s_tok, stream)
+
+
+def w8a8_sandwich_rmsnorm_quant_fp8(y, residual, gamma_smoothed, eps, gamma_post=None,
+                                    eps_post=None, gate=None, res_scale=1.0, h_out=None, q=None,
+                                    s_tok=None, stream=None):
+    """w8a8_sandwich_rmsnorm_quant with FP8 (E4M3) codes."""
+    return _sandwich_quant("w8a8_sandwich_rmsnorm_quant_fp8", FP8, y, residual, gamma_smoothed,
+                           eps, gamma_post, eps_post, gate, res_scale, h_out, q, s_tok, stream)
+
+
+def w8a8_sandwich_rmsnorm_backward_workspace_size(M: int, K: int) -> int:
+    return int(lib().w8a8_sandwich_rmsnorm_backward_workspace_size(M, K))
+
+
+def w8a8_sandwich_rmsnorm_backward(dz, y, h, gamma_smoothed, eps, dh=None, gamma_post=None,
+                                   eps_post=None, gate=None, res_scale=1.0, dy=None,
+                                   dresidual=None, workspace=None, stream=None):
+    """The backward pass of w8a8_sandwich_rmsnorm_quant (either code), the quantization passed
+    straight through: dz bf16 [M, K] is the gradient of the codes' values, dh bf16 [M, K] (or
+    None) the gradient that reaches h by the residual stream, y and h the forward call's input
+    and stored output. dresidual may be dh (in place). Returns (dy, dresidual, dgamma_smoothed,
+    dgamma_post or None, dgate or None), dgate in gate's shape and type."""
+    _need(dz, "dz", torch.bfloat16)
+    if dz.dim() != 2:
+        raise ValueError(f"dz must be [M, K], got {tuple(dz.shape)}")
+    M, K = dz.shape
+    _need(y, "y", torch.bfloat16, (M, K))
+    _need(h, "h", torch.bfloat16, (M, K))
+    if dh is not None:
+        _need(dh, "dh", torch.bfloat16, (M, K))
+    _need(gamma_smoothed, "gamma_smoothed", torch.float32, (K,))
+    if gamma_post is not None:
+        _need(gamma_post, "gamma_post", torch.float32, (K,))
+    kind = _gate_kind(gate, M, K)
+    with _place(dz, stream):
+        dy = torch.empty_like(dz) if dy is None else dy
+        dresidual = torch.empty_like(dz) if dresidual is None else dresidual
+        _need(dy, "dy", torch.bfloat16, (M, K))
+        _need(dresidual, "dresidual", torch.bfloat16, (M, K))
+        _same_device(dz, y=y, h=h, dh=dh, gamma_smoothed=gamma_smoothed, gamma_post=gamma_post,
+                     gate=gate, dy=dy, dresidual=dresidual)
+        dpre = torch.empty_like(gamma_smoothed)
+        dpost = None if gamma_post is None else torch.empty_like(gamma_post)
+        dgate = None if gate is None else torch.empty_like(gate)
+        wptr, wbytes, keep = _scratch(workspace, w8a8_sandwich_rmsnorm_backward_workspace_size(M, K),
+                                      dz.device)
+        _check("w8a8_sandwich_rmsnorm_backward", lib().w8a8_sandwich_rmsnorm_backward(
+            _ptr(dz), _ptr(dh), _ptr(y), _ptr(h), _ptr(gamma_post),
+            float(eps if eps_post is None else eps_post), _ptr(gate), kind, float(res_scale),
+            _ptr(gamma_smoothed), float(eps), M, K, _ptr(dy), _ptr(dresidual), _ptr(dpost),
+            _ptr(dgate), _ptr(dpre), wptr, wbytes, _stream(None)))
+        del keep
+    return dy, dresidual, dpre, dpost, dgate

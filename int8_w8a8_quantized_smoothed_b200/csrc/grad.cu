@@ -1,0 +1,284 @@
+// C ABI of the block-boundary norms and of the W8A8 linear's gradients (declared in
+// include/w8a8.h): argument validation, launch shapes and launches. The kernels are in
+// sandwich.cuh and gradgemm.cuh.
+#include "host.cuh"
+#include "sandwich.cuh"
+
+#include <algorithm>
+
+namespace w8a8 {
+
+cudaError_t grad_status_read(unsigned int *word, cudaStream_t st)
+{
+    return cudaMemcpyFromSymbolAsync(word, g_status_word, sizeof(*word), 0, cudaMemcpyDeviceToHost,
+                                     st);
+}
+
+cudaError_t grad_status_clear()
+{
+    const unsigned int zero = 0;
+    return cudaMemcpyToSymbol(g_status_word, &zero, sizeof(zero));
+}
+
+} // namespace w8a8
+
+namespace {
+
+using namespace w8a8;
+
+bool same(const void *a, const void *b)
+{
+    return a != nullptr && a == b;
+}
+
+// ------------------------------------------------------------------ norms at a block boundary
+
+struct SandwichArgs {
+    const uint16_t *y, *res;
+    const float *gamma_post;
+    const void *gate;
+    float res_scale;
+    const float *gamma_pre;
+    float eps_post, eps_pre;
+    int64_t M;
+    int K;
+    uint16_t *h;
+    int8_t *q;
+    float *s;
+};
+
+template <int NCH, bool POST, int GATE, bool F8>
+int launch_sandwich(const SandwichArgs &a, int threads, int dev, int sms, cudaStream_t st)
+{
+    const void *fn = reinterpret_cast<const void *>(&sandwich_quant_kernel<NCH, POST, GATE, F8>);
+    if (int rc = ensure_smem(fn, dev, 0))
+        return rc;
+    return launch_kernel(sandwich_quant_kernel<NCH, POST, GATE, F8>,
+                         dim3(row_grid(fn, threads, a.M, dev, sms)), dim3(threads), 0, st, a.y,
+                         a.res, a.gamma_post, a.gate, a.res_scale, a.gamma_pre, a.eps_post,
+                         a.eps_pre, a.K, static_cast<int>(a.M), a.h, a.q, a.s);
+}
+
+template <int NCH, bool POST, bool F8>
+int launch_sandwich_gate(const SandwichArgs &a, int gate_kind, int threads, int dev, int sms,
+                         cudaStream_t st)
+{
+    switch (gate_kind) {
+    case kGateFull: return launch_sandwich<NCH, POST, kGateFull, F8>(a, threads, dev, sms, st);
+    case kGateChannel: return launch_sandwich<NCH, POST, kGateChannel, F8>(a, threads, dev, sms, st);
+    default: return launch_sandwich<NCH, POST, kGateToken, F8>(a, threads, dev, sms, st);
+    }
+}
+
+template <int NCH, bool F8>
+int launch_sandwich_post(const SandwichArgs &a, int gate_kind, int threads, int dev, int sms,
+                         cudaStream_t st)
+{
+    if (a.gamma_post)
+        return launch_sandwich_gate<NCH, true, F8>(a, gate_kind, threads, dev, sms, st);
+    return launch_sandwich_gate<NCH, false, F8>(a, gate_kind, threads, dev, sms, st);
+}
+
+bool gate_args_ok(const void *gate, int gate_kind)
+{
+    return gate_kind >= W8A8_GATE_NONE && gate_kind <= W8A8_GATE_FULL &&
+           (gate != nullptr) == (gate_kind != W8A8_GATE_NONE);
+}
+
+bool finite(float v)
+{
+    return v - v == 0.0f;
+}
+
+template <bool F8>
+int sandwich_quant_impl(const uint16_t *y, const uint16_t *residual, const float *gamma_post,
+                        float eps_post, const void *gate, int gate_kind, float res_scale,
+                        const float *gamma_smoothed, float eps, int64_t M, int64_t K,
+                        uint16_t *h_out, int8_t *q, float *s_tok, w8a8_stream_t stream)
+{
+    if (!y || !residual || !gamma_smoothed || !h_out || !q || !s_tok ||
+        !gate_args_ok(gate, gate_kind) || !finite(res_scale) || !(eps >= 0.0f) ||
+        (gamma_post && !(eps_post >= 0.0f)))
+        return W8A8_ERR_INVALID_ARG;
+    int rc = check_row_shape(M, K);
+    if (rc)
+        return rc;
+    if (!aligned16(y) || !aligned16(residual) || !aligned16(gamma_smoothed) || !aligned16(h_out) ||
+        !aligned16(q) || (gamma_post && !aligned16(gamma_post)) ||
+        (gate_kind >= W8A8_GATE_CHANNEL && !aligned16(gate)))
+        return W8A8_ERR_ALIGNMENT;
+    if (same(h_out, y) || same(h_out, gate) || same(q, y) || same(q, residual) || same(q, h_out) ||
+        same(q, gate))
+        return W8A8_ERR_INVALID_ARG;
+    int dev, sms;
+    if ((rc = current_device(&dev, &sms)))
+        return rc;
+    const SandwichArgs a{y, residual, gamma_post, gate, res_scale, gamma_smoothed, eps_post, eps,
+                         M, static_cast<int>(K), h_out, q, s_tok};
+    const RowLaunch L = row_launch(K);
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    switch (L.nch) {
+    case 1: return launch_sandwich_post<1, F8>(a, gate_kind, L.threads, dev, sms, st);
+    case 2: return launch_sandwich_post<2, F8>(a, gate_kind, L.threads, dev, sms, st);
+    default: return launch_sandwich_post<4, F8>(a, gate_kind, L.threads, dev, sms, st);
+    }
+}
+
+// Backward launch shape: clusters of `csize` CTAs of `threads`, one vector of 8 columns per
+// thread; as many clusters as the device holds at 128 registers a thread, never more than rows.
+struct SandwichBackPlan {
+    int csize, threads;
+    int64_t clusters;
+    size_t ws_bytes;
+};
+
+SandwichBackPlan sandwich_back_plan(int64_t M, int64_t K, int sms)
+{
+    SandwichBackPlan p;
+    const int64_t nvec = K / 8;
+    p.csize = static_cast<int>((nvec + kBackMaxThreads - 1) / kBackMaxThreads);
+    const int64_t per = (nvec + p.csize - 1) / p.csize;
+    p.threads = static_cast<int>((per + 31) / 32 * 32);
+    const int64_t resident = static_cast<int64_t>(sms) * (kBackMaxThreads / p.threads) / p.csize;
+    p.clusters = std::max<int64_t>(1, std::min<int64_t>(M, resident));
+    p.ws_bytes = static_cast<size_t>(p.clusters) * 2 * static_cast<size_t>(K) * sizeof(float);
+    return p;
+}
+
+template <bool POST, int GATE>
+int launch_sandwich_back(const SandwichBack &a, const SandwichBackPlan &p, int dev, cudaStream_t st)
+{
+    if (p.csize > 1) {
+        const void *fn = reinterpret_cast<const void *>(&sandwich_back_kernel<POST, GATE, true>);
+        if (int rc = ensure_smem(fn, dev, 0))
+            return rc;
+        return launch_kernel_cluster(sandwich_back_kernel<POST, GATE, true>,
+                                     dim3(static_cast<unsigned>(p.clusters * p.csize)),
+                                     dim3(p.threads), 0, st, static_cast<unsigned>(p.csize), a);
+    }
+    const void *fn = reinterpret_cast<const void *>(&sandwich_back_kernel<POST, GATE, false>);
+    if (int rc = ensure_smem(fn, dev, 0))
+        return rc;
+    return launch_kernel(sandwich_back_kernel<POST, GATE, false>,
+                         dim3(static_cast<unsigned>(p.clusters)), dim3(p.threads), 0, st, a);
+}
+
+template <bool POST>
+int launch_sandwich_back_gate(const SandwichBack &a, int gate_kind, const SandwichBackPlan &p,
+                              int dev, cudaStream_t st)
+{
+    switch (gate_kind) {
+    case W8A8_GATE_FULL: return launch_sandwich_back<POST, kGateFull>(a, p, dev, st);
+    case W8A8_GATE_CHANNEL: return launch_sandwich_back<POST, kGateChannel>(a, p, dev, st);
+    default: return launch_sandwich_back<POST, kGateToken>(a, p, dev, st);
+    }
+}
+
+} // namespace
+
+extern "C" {
+
+int w8a8_sandwich_rmsnorm_quant(const w8a8_bf16 *y, const w8a8_bf16 *residual,
+                                const float *gamma_post, float eps_post, const void *gate,
+                                int gate_kind, float res_scale, const float *gamma_smoothed,
+                                float eps, int64_t M, int64_t K, w8a8_bf16 *h_out, int8_t *q,
+                                float *s_tok, w8a8_stream_t stream)
+{
+    return sandwich_quant_impl<false>(y, residual, gamma_post, eps_post, gate, gate_kind,
+                                      res_scale, gamma_smoothed, eps, M, K, h_out, q, s_tok,
+                                      stream);
+}
+
+int w8a8_sandwich_rmsnorm_quant_fp8(const w8a8_bf16 *y, const w8a8_bf16 *residual,
+                                    const float *gamma_post, float eps_post, const void *gate,
+                                    int gate_kind, float res_scale, const float *gamma_smoothed,
+                                    float eps, int64_t M, int64_t K, w8a8_bf16 *h_out, uint8_t *q,
+                                    float *s_tok, w8a8_stream_t stream)
+{
+    return sandwich_quant_impl<true>(y, residual, gamma_post, eps_post, gate, gate_kind, res_scale,
+                                     gamma_smoothed, eps, M, K, h_out,
+                                     reinterpret_cast<int8_t *>(q), s_tok, stream);
+}
+
+size_t w8a8_sandwich_rmsnorm_backward_workspace_size(int64_t M, int64_t K)
+{
+    if (check_row_shape(M, K))
+        return 0;
+    int dev, sms = 148;
+    if (current_device(&dev, &sms))
+        sms = 148;
+    return sandwich_back_plan(M, K, sms).ws_bytes;
+}
+
+int w8a8_sandwich_rmsnorm_backward(const w8a8_bf16 *dz, const w8a8_bf16 *dh, const w8a8_bf16 *y,
+                                   const w8a8_bf16 *h, const float *gamma_post, float eps_post,
+                                   const void *gate, int gate_kind, float res_scale,
+                                   const float *gamma_smoothed, float eps, int64_t M, int64_t K,
+                                   w8a8_bf16 *dy, w8a8_bf16 *dresidual, float *dgamma_post,
+                                   void *dgate, float *dgamma_smoothed, void *workspace,
+                                   size_t workspace_bytes, w8a8_stream_t stream)
+{
+    if (!dz || !y || !h || !gamma_smoothed || !dy || !dresidual || !dgamma_smoothed ||
+        !gate_args_ok(gate, gate_kind) || (dgate != nullptr) != (gate != nullptr) ||
+        (dgamma_post != nullptr) != (gamma_post != nullptr) || !finite(res_scale) ||
+        !(eps >= 0.0f) || (gamma_post && !(eps_post >= 0.0f)))
+        return W8A8_ERR_INVALID_ARG;
+    int rc = check_row_shape(M, K);
+    if (rc)
+        return rc;
+    if (!aligned16(dz) || (dh && !aligned16(dh)) || !aligned16(y) || !aligned16(h) ||
+        !aligned16(gamma_smoothed) || (gamma_post && !aligned16(gamma_post)) || !aligned16(dy) ||
+        !aligned16(dresidual) || (workspace && !aligned16(workspace)) ||
+        (gate_kind >= W8A8_GATE_CHANNEL && !aligned16(gate)) ||
+        (gate_kind == W8A8_GATE_FULL && !aligned16(dgate)))
+        return W8A8_ERR_ALIGNMENT;
+    // dresidual may be dh (in place); every other output is written while inputs are still read
+    const void *in[] = {dz, y, h, gate};
+    for (const void *p : in)
+        if (same(dy, p) || same(dresidual, p) || same(dgate, p))
+            return W8A8_ERR_INVALID_ARG;
+    if (same(dy, dh) || same(dgate, dh) || same(dy, dresidual) || same(dgate, dy) ||
+        same(dgate, dresidual))
+        return W8A8_ERR_INVALID_ARG;
+    int dev, sms;
+    if ((rc = current_device(&dev, &sms)))
+        return rc;
+    const SandwichBackPlan p = sandwich_back_plan(M, K, sms);
+    if (workspace == nullptr || workspace_bytes < p.ws_bytes)
+        return W8A8_ERR_WORKSPACE;
+    SandwichBack a;
+    a.dz = dz;
+    a.dh = dh;
+    a.y = y;
+    a.h = h;
+    a.gamma_post = gamma_post;
+    a.gamma_pre = gamma_smoothed;
+    a.gate = gate;
+    a.dy = dy;
+    a.dres = dresidual;
+    a.dgate_full = gate_kind == W8A8_GATE_FULL ? static_cast<uint16_t *>(dgate) : nullptr;
+    a.dgate_tok = gate_kind == W8A8_GATE_TOKEN ? static_cast<float *>(dgate) : nullptr;
+    a.part = static_cast<float *>(workspace);
+    a.res_scale = res_scale;
+    a.eps_post = eps_post;
+    a.eps_pre = eps;
+    a.K = static_cast<int>(K);
+    a.M = static_cast<int>(M);
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    rc = gamma_post ? launch_sandwich_back_gate<true>(a, gate_kind, p, dev, st)
+                    : launch_sandwich_back_gate<false>(a, gate_kind, p, dev, st);
+    if (rc)
+        return rc;
+    const bool channel = gate_kind == W8A8_GATE_CHANNEL;
+    const void *fn = reinterpret_cast<const void *>(&sandwich_part_kernel);
+    if ((rc = ensure_smem(fn, dev, 0)))
+        return rc;
+    return launch_kernel(sandwich_part_kernel,
+                         dim3(static_cast<unsigned>((K + 31) / 32), gamma_post || channel ? 2 : 1),
+                         dim3(256), 0, st, static_cast<const float *>(workspace),
+                         static_cast<int>(p.clusters), static_cast<int>(K), gamma_post,
+                         channel ? static_cast<const float *>(gate) : nullptr, dgamma_smoothed,
+                         dgamma_post, channel ? static_cast<float *>(dgate) : nullptr);
+}
+
+} // extern "C"

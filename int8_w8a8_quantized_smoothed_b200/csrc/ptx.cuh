@@ -9,7 +9,8 @@
 namespace w8a8 {
 
 // Set by any kernel whose bounded wait ran out; read and cleared by w8a8_device_status().
-__device__ unsigned int g_status_word;
+// Each translation unit has its own word.
+static __device__ unsigned int g_status_word;
 
 constexpr unsigned int kStatusTimeout = 1u;
 

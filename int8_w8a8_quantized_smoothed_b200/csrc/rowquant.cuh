@@ -340,7 +340,7 @@ __global__ void __launch_bounds__(NCH <= 2 ? 256 : 1024, NCH <= 2 ? 6 : 1) quant
 // kernel is a grid-stride pass over the 8-value vectors of all rows (HBM-bound). Values
 // beyond the calibrated range saturate at +-127.
 
-__global__ void __launch_bounds__(256) quantize_rows_static_kernel(
+static __global__ void __launch_bounds__(256) quantize_rows_static_kernel(
     const uint16_t *__restrict__ x, const float *__restrict__ sinv, float S, int K,
     int64_t nvec_total, int M, int8_t *__restrict__ q, float *__restrict__ s_tok)
 {
