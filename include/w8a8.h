@@ -373,6 +373,59 @@ W8A8_API int w8a8_sandwich_rmsnorm_backward(const w8a8_bf16 *dz, const w8a8_bf16
                                             size_t workspace_bytes, w8a8_stream_t stream);
 
 /*
+ * ---------------------------------------------------------------- gradients of a W8A8 linear
+ *
+ * The backward pass of w8a8_gemm_dequant (and of its FP8 form) with the codes held fixed, or
+ * passed straight through to the weight they were rounded from, and of the gated feed-forward
+ * block built on it: the step from calibration to tuning a quantized block [W8A8 "The solution:
+ * How GPTQ improves on naive quantization" adjusts weights to the rounding error without
+ * gradients; gradients are not on the pages]. With wd = bf16(wq s_ch) and xd = bf16(xq s_tok), the
+ * dequantized operand rounded once:
+ *   w8a8_gemm_dgrad       dx[m,k] = bf16(sum_n dy[m,n] wd[n,k])
+ *   w8a8_gemm_wgrad       dw[n,k] = bf16(sum_m dy[m,n] xd[m,k])
+ *   w8a8_gemm_dgrad_silu  the down projection's input gradient, continued through
+ *                         a = silu(g) u [the product the down projection reads]:
+ *                           da[m,i]         = sum_n dy[m,n] wd[n,i]          (binary32, not stored)
+ *                           dgate_up[m,i]   = bf16(da u sig (1 + g (1 - sig))), sig = 1/(1+exp(-g))
+ *                           dgate_up[m,I+i] = bf16(da g sig)
+ * Sums of bf16 products in binary32 on the tensor cores (kind::f16). INT8 scales enter with 15
+ * significant bits (2^-16 relative). A long sum may be split between SMs, its parts added in a
+ * fixed order: the same call gives the same bits on the same device.
+ * dy: bf16 [M,N], the gradient of the linear's output (N of the down projection: the hidden
+ * size). wq [N,K] and s_ch fp32 [N]: the forward call's weight; xq [M,K] and s_tok fp32 [M]: its
+ * activations; codes as int8, or E4M3 as uint8 (_fp8). gate_up: bf16 [M,2I], the forward gate|up
+ * output ([gate | up] halves, as w8a8_silu_mul_quant reads it); dgate_up likewise. For the gate|up
+ * projection itself the rows of wq and the columns of dy only have to agree, so the interleaved
+ * weight of w8a8_gemm_silu_quant serves with dy interleaved alike. dx: bf16 [M,K]; dw: bf16 [N,K].
+ * Every matrix 16-byte aligned; no output may alias an input. Scales finite, below 2^100.
+ * Requires M >= 1, N >= 8, N % 8 == 0, K (I) >= 16, K % 16 == 0, each at most 2^30.
+ * workspace: w8a8_gemm_dgrad_workspace_size(M, N, K) bytes (dgrad_silu: K = I), or
+ * w8a8_gemm_wgrad_workspace_size(M, N, K), 16-byte aligned, any contents (0: may be NULL).
+ */
+W8A8_API size_t w8a8_gemm_dgrad_workspace_size(int64_t M, int64_t N, int64_t K);
+W8A8_API size_t w8a8_gemm_wgrad_workspace_size(int64_t M, int64_t N, int64_t K);
+W8A8_API int w8a8_gemm_dgrad(const w8a8_bf16 *dy, const int8_t *wq, const float *s_ch, int64_t M,
+                             int64_t N, int64_t K, w8a8_bf16 *dx, void *workspace,
+                             size_t workspace_bytes, w8a8_stream_t stream);
+W8A8_API int w8a8_gemm_dgrad_fp8(const w8a8_bf16 *dy, const uint8_t *wq, const float *s_ch,
+                                 int64_t M, int64_t N, int64_t K, w8a8_bf16 *dx, void *workspace,
+                                 size_t workspace_bytes, w8a8_stream_t stream);
+W8A8_API int w8a8_gemm_dgrad_silu(const w8a8_bf16 *dy, const int8_t *wq, const float *s_ch,
+                                  int64_t M, int64_t N, int64_t I, const w8a8_bf16 *gate_up,
+                                  w8a8_bf16 *dgate_up, void *workspace, size_t workspace_bytes,
+                                  w8a8_stream_t stream);
+W8A8_API int w8a8_gemm_dgrad_silu_fp8(const w8a8_bf16 *dy, const uint8_t *wq, const float *s_ch,
+                                      int64_t M, int64_t N, int64_t I, const w8a8_bf16 *gate_up,
+                                      w8a8_bf16 *dgate_up, void *workspace,
+                                      size_t workspace_bytes, w8a8_stream_t stream);
+W8A8_API int w8a8_gemm_wgrad(const w8a8_bf16 *dy, const int8_t *xq, const float *s_tok, int64_t M,
+                             int64_t N, int64_t K, w8a8_bf16 *dw, void *workspace,
+                             size_t workspace_bytes, w8a8_stream_t stream);
+W8A8_API int w8a8_gemm_wgrad_fp8(const w8a8_bf16 *dy, const uint8_t *xq, const float *s_tok,
+                                 int64_t M, int64_t N, int64_t K, w8a8_bf16 *dw, void *workspace,
+                                 size_t workspace_bytes, w8a8_stream_t stream);
+
+/*
  * ---------------------------------------------------------------- the fused decoder block
  *
  * One Llama decoder block's whole linear path at decode sizes (1 <= M <= 64 tokens) as a single

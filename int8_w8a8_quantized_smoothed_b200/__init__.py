@@ -32,6 +32,9 @@ __all__ = [
     "w8a8_gptq_quantize", "w8a8_gptq_workspace_size", "w8a8_probe_f64_fma",
     "w8a8_block_decode", "w8a8_block_decode_workspace_size", "BlockBuffers",
     "w8a8_sandwich_rmsnorm_quant", "w8a8_sandwich_rmsnorm_quant_fp8",
+    "w8a8_gemm_dgrad", "w8a8_gemm_dgrad_fp8", "w8a8_gemm_dgrad_silu", "w8a8_gemm_dgrad_silu_fp8",
+    "w8a8_gemm_wgrad", "w8a8_gemm_wgrad_fp8", "w8a8_gemm_dgrad_workspace_size",
+    "w8a8_gemm_wgrad_workspace_size",
     "w8a8_sandwich_rmsnorm_backward", "w8a8_sandwich_rmsnorm_backward_workspace_size",
     "Workspace", "FP8",
 ]
@@ -90,6 +93,12 @@ SIGNATURES = [
     ("w8a8_sandwich_rmsnorm_backward_workspace_size", _SZ, [_I64, _I64]),
     ("w8a8_sandwich_rmsnorm_backward", _I, [_P, _P, _P, _P, _P, _F, _P, _I, _F, _P, _F, _I64,
                                             _I64, _P, _P, _P, _P, _P, _P, _SZ, _P]),
+    ("w8a8_gemm_dgrad_workspace_size", _SZ, [_I64, _I64, _I64]),
+    ("w8a8_gemm_wgrad_workspace_size", _SZ, [_I64, _I64, _I64]),
+    *[(f"w8a8_gemm_{g}{f}", _I, [_P, _P, _P, _I64, _I64, _I64, _P, _P, _SZ, _P])
+      for g in ("dgrad", "wgrad") for f in ("", "_fp8")],
+    *[(f"w8a8_gemm_dgrad_silu{f}", _I, [_P, _P, _P, _I64, _I64, _I64, _P, _P, _P, _SZ, _P])
+      for f in ("", "_fp8")],
     ("w8a8_probe_f64_fma", _I, [C.c_longlong, _I, _P, _P]),
     ("w8a8_gptq_quantize", _I, [_P, _P, _P, _I64, _I64, _I64, C.c_double, _P, _P, _P, _P, _SZ,
                                 _P]),
@@ -846,3 +855,83 @@ def w8a8_sandwich_rmsnorm_backward(dz, y, h, gamma_smoothed, eps, dh=None, gamma
             _ptr(dgate), _ptr(dpre), wptr, wbytes, _stream(None)))
         del keep
     return dy, dresidual, dpre, dpost, dgate
+
+
+def w8a8_gemm_dgrad_workspace_size(M: int, N: int, K: int) -> int:
+    return int(lib().w8a8_gemm_dgrad_workspace_size(M, N, K))
+
+
+def w8a8_gemm_wgrad_workspace_size(M: int, N: int, K: int) -> int:
+    return int(lib().w8a8_gemm_wgrad_workspace_size(M, N, K))
+
+
+def _grad(name, code, dy, q, scale, rows, out, out_name, gate_up, workspace, stream):
+    """rows: which of dy's dimensions the code matrix q has as its rows (1: N, the weight; 0: M,
+    the activations)."""
+    _need(dy, "dy", torch.bfloat16)
+    if dy.dim() != 2:
+        raise ValueError(f"dy must be [M, N], got {tuple(dy.shape)}")
+    M, N = dy.shape
+    qn, sn = ("wq", "s_ch") if rows else ("xq", "s_tok")
+    _need(q, qn, code)
+    if q.dim() != 2 or q.shape[0] != dy.shape[rows]:
+        raise ValueError(f"{qn} must be [{dy.shape[rows]}, K] for dy {tuple(dy.shape)}, got "
+                         f"{tuple(q.shape)}")
+    K = q.shape[1]
+    _need(scale, sn, torch.float32, (dy.shape[rows],))
+    shape = (M, K) if rows else (N, K)
+    if gate_up is not None:
+        shape = (M, 2 * K)
+        _need(gate_up, "gate_up", torch.bfloat16, shape)
+    with _place(dy, stream):
+        out = torch.empty(shape, dtype=torch.bfloat16, device=dy.device) if out is None else out
+        _need(out, out_name, torch.bfloat16, shape)
+        _same_device(dy, **{qn: q, sn: scale, "gate_up": gate_up, out_name: out})
+        size = w8a8_gemm_dgrad_workspace_size if rows else w8a8_gemm_wgrad_workspace_size
+        wptr, wbytes, keep = _scratch(workspace, size(M, N, K), dy.device)
+        extra = () if gate_up is None else (_ptr(gate_up),)
+        _check(name, getattr(lib(), name)(_ptr(dy), _ptr(q), _ptr(scale), M, N, K, *extra,
+                                          _ptr(out), wptr, wbytes, _stream(None)))
+        del keep
+    return out
+
+
+def w8a8_gemm_dgrad(dy, wq, s_ch, dx=None, workspace=None, stream=None):
+    """Input gradient of a W8A8 linear: dx [M, K] = dy [M, N] @ (wq * s_ch[:, None]) in bf16, the
+    weight's int8 codes dequantized inside the kernel."""
+    return _grad("w8a8_gemm_dgrad", torch.int8, dy, wq, s_ch, 1, dx, "dx", None, workspace, stream)
+
+
+def w8a8_gemm_dgrad_fp8(dy, wq, s_ch, dx=None, workspace=None, stream=None):
+    """w8a8_gemm_dgrad with FP8 (E4M3) weight codes."""
+    return _grad("w8a8_gemm_dgrad_fp8", FP8, dy, wq, s_ch, 1, dx, "dx", None, workspace, stream)
+
+
+def w8a8_gemm_dgrad_silu(dy, wq, s_ch, gate_up, dgate_up=None, workspace=None, stream=None):
+    """The gated feed-forward block's backward step: da = dy [M, H] @ (wq * s_ch[:, None]) with the
+    down projection's wq [H, I], then the gradients of silu(gate) * up from the forward gate|up
+    values gate_up [M, 2I]. Returns dgate_up [M, 2I]; da is not stored."""
+    if gate_up is None:
+        raise TypeError("gate_up must be a torch.Tensor")
+    return _grad("w8a8_gemm_dgrad_silu", torch.int8, dy, wq, s_ch, 1, dgate_up, "dgate_up",
+                 gate_up, workspace, stream)
+
+
+def w8a8_gemm_dgrad_silu_fp8(dy, wq, s_ch, gate_up, dgate_up=None, workspace=None, stream=None):
+    """w8a8_gemm_dgrad_silu with FP8 (E4M3) weight codes."""
+    if gate_up is None:
+        raise TypeError("gate_up must be a torch.Tensor")
+    return _grad("w8a8_gemm_dgrad_silu_fp8", FP8, dy, wq, s_ch, 1, dgate_up, "dgate_up", gate_up,
+                 workspace, stream)
+
+
+def w8a8_gemm_wgrad(dy, xq, s_tok, dw=None, workspace=None, stream=None):
+    """Weight gradient of a W8A8 linear, passed straight through the weight's rounding: dw [N, K] =
+    dy [M, N]^T @ (xq * s_tok[:, None]) in bf16, the activations' int8 codes dequantized inside
+    the kernel."""
+    return _grad("w8a8_gemm_wgrad", torch.int8, dy, xq, s_tok, 0, dw, "dw", None, workspace, stream)
+
+
+def w8a8_gemm_wgrad_fp8(dy, xq, s_tok, dw=None, workspace=None, stream=None):
+    """w8a8_gemm_wgrad with FP8 (E4M3) activation codes."""
+    return _grad("w8a8_gemm_wgrad_fp8", FP8, dy, xq, s_tok, 0, dw, "dw", None, workspace, stream)

@@ -1,6 +1,7 @@
 // C ABI of the block-boundary norms and of the W8A8 linear's gradients (declared in
 // include/w8a8.h): argument validation, launch shapes and launches. The kernels are in
 // sandwich.cuh and gradgemm.cuh.
+#include "gradgemm.cuh"
 #include "host.cuh"
 #include "sandwich.cuh"
 
@@ -174,9 +175,197 @@ int launch_sandwich_back_gate(const SandwichBack &a, int gate_kind, const Sandwi
     }
 }
 
+// ------------------------------------------------------------------ gradients of a W8A8 linear
+
+constexpr int kGradStages = 5, kGradQStages = 4;
+// A pair takes at least this many k-blocks of a split tile: below it the partial tile's store and
+// the addition cost more than the k-blocks.
+constexpr int64_t kGradMinSplit = 8;
+
+int check_grad_shape(int64_t M, int64_t N, int64_t K)
+{
+    if (M < 1 || N < 8 || K < 16)
+        return W8A8_ERR_INVALID_ARG;
+    if (N % 8 != 0 || K % 16 != 0 || M > (1 << 30) || N > (1 << 30) || K > (1 << 30))
+        return W8A8_ERR_UNSUPPORTED_SHAPE;
+    return W8A8_OK;
+}
+
+// False when there are more tiles than an int counts.
+bool grad_work(int64_t I, int64_t J, int64_t R, int sms, GradWork *w)
+{
+    const int64_t ni = (I + kGradTile - 1) / kGradTile, nj = (J + kGradTile - 1) / kGradTile;
+    const int64_t tiles = ni * nj, kb = (R + kGradBR - 1) / kGradBR, pairs = sms / 2;
+    if (tiles > (1 << 30))
+        return false;
+    w->I = static_cast<int>(I);
+    w->J = static_cast<int>(J);
+    w->R = static_cast<int>(R);
+    w->ni = static_cast<int>(ni);
+    w->nj = static_cast<int>(nj);
+    w->kblocks = static_cast<int>(kb);
+    w->group_i = 8;
+    w->npairs = static_cast<int>(pairs);
+    w->whole = static_cast<int>(tiles / pairs * pairs);
+    w->rem = static_cast<int>(tiles % pairs);
+    w->rem_pairs = static_cast<int>(
+        w->rem == 0 ? 0 : std::min(pairs, std::max<int64_t>(w->rem, w->rem * kb / kGradMinSplit)));
+    return true;
+}
+
+size_t grad_ws_bytes(const GradWork &w)
+{
+    return w.rem_pairs > w.rem
+               ? static_cast<size_t>(w.rem_pairs) * 2 * kGradTile * kGradTile * sizeof(float)
+               : 0;
+}
+
+// 2-D row-major tensor, `inner` elements of `esize` bytes per row, 128-byte boxes.
+int encode_grad(CUtensorMap *map, const void *base, int64_t rows, int64_t inner, int esize,
+                int box_rows, bool swizzle)
+{
+    cuuint64_t dims[2] = {static_cast<cuuint64_t>(inner), static_cast<cuuint64_t>(rows)};
+    cuuint64_t strides[1] = {static_cast<cuuint64_t>(inner * esize)};
+    cuuint32_t box[2] = {static_cast<cuuint32_t>(128 / esize), static_cast<cuuint32_t>(box_rows)};
+    cuuint32_t estr[2] = {1, 1};
+    CUresult r = g_encode(map,
+                          esize == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8,
+                          2, const_cast<void *>(base), dims, strides, box, estr,
+                          CU_TENSOR_MAP_INTERLEAVE_NONE,
+                          swizzle ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
+                          CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? W8A8_OK : W8A8_ERR_CUDA;
+}
+
+template <bool WGRAD, bool F8, bool SILU>
+int launch_grad(const CUtensorMap &ta, const CUtensorMap &tq, const float *scale,
+                const GradWork &w, const uint16_t *gate_up, uint16_t *out, float *part, int dev,
+                cudaStream_t st)
+{
+    using Cfg = GradCfg<kGradStages, kGradQStages>;
+    auto kernel = grad_gemm_kernel<kGradStages, kGradQStages, WGRAD, F8, SILU>;
+    if (int rc = ensure_smem(reinterpret_cast<const void *>(kernel), dev, Cfg::kSmemBytes))
+        return rc;
+    const unsigned pairs = static_cast<unsigned>(w.whole > 0 ? w.npairs : w.rem_pairs);
+    if (int rc = launch_kernel_cluster(kernel, dim3(2 * pairs), dim3(kGradThreads), Cfg::kSmemBytes,
+                                       st, 2u, ta, tq, scale, w, gate_up, out, part, kWaitLimitNs))
+        return rc;
+    if (w.rem_pairs <= w.rem)
+        return W8A8_OK; // no tile was split
+    const void *fix = reinterpret_cast<const void *>(&grad_fixup_kernel<SILU>);
+    if (int rc = ensure_smem(fix, dev, 0))
+        return rc;
+    const unsigned rows = static_cast<unsigned>(std::min(w.I, kGradTile));
+    return launch_kernel(grad_fixup_kernel<SILU>, dim3((rows + 7) / 8, static_cast<unsigned>(w.rem)),
+                         dim3(256), 0, st, w, static_cast<const float *>(part), gate_up, out);
+}
+
+// dy [M, N]; Q: wq [N, K] (input gradient) or xq [M, K] (weight gradient).
+template <bool WGRAD, bool SILU>
+int grad_impl(bool f8, const uint16_t *dy, const void *q, const float *scale, int64_t M, int64_t N,
+              int64_t K, const uint16_t *gate_up, uint16_t *out, void *workspace,
+              size_t workspace_bytes, w8a8_stream_t stream)
+{
+    if (!dy || !q || !scale || !out || (SILU && !gate_up))
+        return W8A8_ERR_INVALID_ARG;
+    int rc = check_grad_shape(M, N, K);
+    if (rc)
+        return rc;
+    if (!aligned16(dy) || !aligned16(q) || !aligned16(out) || (SILU && !aligned16(gate_up)) ||
+        (workspace && !aligned16(workspace)))
+        return W8A8_ERR_ALIGNMENT;
+    if (same(out, dy) || same(out, q) || same(out, gate_up))
+        return W8A8_ERR_INVALID_ARG;
+    int dev, sms;
+    if ((rc = current_device(&dev, &sms)))
+        return rc;
+    GradWork w;
+    if (!grad_work(WGRAD ? N : M, K, WGRAD ? M : N, sms, &w))
+        return W8A8_ERR_UNSUPPORTED_SHAPE;
+    if (grad_ws_bytes(w) > 0 && (workspace == nullptr || workspace_bytes < grad_ws_bytes(w)))
+        return W8A8_ERR_WORKSPACE;
+    CUtensorMap ta, tq;
+    if (encode_grad(&ta, dy, M, N, 2, WGRAD ? kGradBR : 128, true) ||
+        encode_grad(&tq, q, WGRAD ? M : N, K, 1, kGradBR, false))
+        return W8A8_ERR_CUDA;
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    float *part = static_cast<float *>(workspace);
+    return f8 ? launch_grad<WGRAD, true, SILU>(ta, tq, scale, w, gate_up, out, part, dev, st)
+              : launch_grad<WGRAD, false, SILU>(ta, tq, scale, w, gate_up, out, part, dev, st);
+}
+
+size_t grad_workspace(int64_t M, int64_t N, int64_t K, bool wgrad)
+{
+    if (check_grad_shape(M, N, K))
+        return 0;
+    int dev, sms = 148;
+    if (current_device(&dev, &sms))
+        sms = 148;
+    GradWork w;
+    return grad_work(wgrad ? N : M, K, wgrad ? M : N, sms, &w) ? grad_ws_bytes(w) : 0;
+}
+
 } // namespace
 
 extern "C" {
+
+size_t w8a8_gemm_dgrad_workspace_size(int64_t M, int64_t N, int64_t K)
+{
+    return grad_workspace(M, N, K, false);
+}
+
+size_t w8a8_gemm_wgrad_workspace_size(int64_t M, int64_t N, int64_t K)
+{
+    return grad_workspace(M, N, K, true);
+}
+
+int w8a8_gemm_dgrad(const w8a8_bf16 *dy, const int8_t *wq, const float *s_ch, int64_t M, int64_t N,
+                    int64_t K, w8a8_bf16 *dx, void *workspace, size_t workspace_bytes,
+                    w8a8_stream_t stream)
+{
+    return grad_impl<false, false>(false, dy, wq, s_ch, M, N, K, nullptr, dx, workspace,
+                                   workspace_bytes, stream);
+}
+
+int w8a8_gemm_dgrad_fp8(const w8a8_bf16 *dy, const uint8_t *wq, const float *s_ch, int64_t M,
+                        int64_t N, int64_t K, w8a8_bf16 *dx, void *workspace,
+                        size_t workspace_bytes, w8a8_stream_t stream)
+{
+    return grad_impl<false, false>(true, dy, wq, s_ch, M, N, K, nullptr, dx, workspace,
+                                   workspace_bytes, stream);
+}
+
+int w8a8_gemm_dgrad_silu(const w8a8_bf16 *dy, const int8_t *wq, const float *s_ch, int64_t M,
+                         int64_t N, int64_t I, const w8a8_bf16 *gate_up, w8a8_bf16 *dgate_up,
+                         void *workspace, size_t workspace_bytes, w8a8_stream_t stream)
+{
+    return grad_impl<false, true>(false, dy, wq, s_ch, M, N, I, gate_up, dgate_up, workspace,
+                                  workspace_bytes, stream);
+}
+
+int w8a8_gemm_dgrad_silu_fp8(const w8a8_bf16 *dy, const uint8_t *wq, const float *s_ch, int64_t M,
+                             int64_t N, int64_t I, const w8a8_bf16 *gate_up, w8a8_bf16 *dgate_up,
+                             void *workspace, size_t workspace_bytes, w8a8_stream_t stream)
+{
+    return grad_impl<false, true>(true, dy, wq, s_ch, M, N, I, gate_up, dgate_up, workspace,
+                                  workspace_bytes, stream);
+}
+
+int w8a8_gemm_wgrad(const w8a8_bf16 *dy, const int8_t *xq, const float *s_tok, int64_t M, int64_t N,
+                    int64_t K, w8a8_bf16 *dw, void *workspace, size_t workspace_bytes,
+                    w8a8_stream_t stream)
+{
+    return grad_impl<true, false>(false, dy, xq, s_tok, M, N, K, nullptr, dw, workspace,
+                                  workspace_bytes, stream);
+}
+
+int w8a8_gemm_wgrad_fp8(const w8a8_bf16 *dy, const uint8_t *xq, const float *s_tok, int64_t M,
+                        int64_t N, int64_t K, w8a8_bf16 *dw, void *workspace,
+                        size_t workspace_bytes, w8a8_stream_t stream)
+{
+    return grad_impl<true, false>(true, dy, xq, s_tok, M, N, K, nullptr, dw, workspace,
+                                  workspace_bytes, stream);
+}
 
 int w8a8_sandwich_rmsnorm_quant(const w8a8_bf16 *y, const w8a8_bf16 *residual,
                                 const float *gamma_post, float eps_post, const void *gate,

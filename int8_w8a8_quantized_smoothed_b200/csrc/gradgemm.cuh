@@ -1,0 +1,631 @@
+// The gradients of a W8A8 linear on the 5th-generation tensor cores (tcgen05.mma kind::f16, bf16
+// operands, binary32 accumulators):
+//
+//   C[i, j] = sum_r A(i, r) B(r, j),   B(r, j) = bf16(s[r] Q[r, j])
+//
+//   input gradient   i = token,   r = output channel, j = input channel:  A = dy, Q = wq, s = s_ch
+//   weight gradient  i = output channel, r = token,   j = input channel:  A = dy^T, Q = xq, s = s_tok
+//
+// Both sum over the rows of the 8-bit matrix Q, which is the dimension its scales belong to, so
+// the scale cannot wait for the epilogue: warps of the kernel turn Q's tiles into scaled bf16
+// tiles in shared memory (a weight is read from HBM as one byte and never stored as two). The
+// codes are exact in bf16; the product with the scale is rounded once. B's tiles keep Q's layout
+// (rows r, j contiguous: the MMA's MN-major form), as does A in the weight gradient (dy's rows
+// are r), so nothing is transposed in memory.
+#pragma once
+
+#include "gemm.cuh"
+
+namespace w8a8 {
+
+constexpr int kGradThreads = 512; // A producer, MMA, 4 epilogue, Q producer, idle, 8 converters
+constexpr int kGradConvWarp0 = 8;
+constexpr int kGradConvWarps = 8;
+constexpr int kGradTile = 256; // rows i and columns j of a pair's tile
+constexpr int kGradBR = 64;    // r per k-block: one 128-byte row of bf16
+
+// Tiles [0, whole) go to the pairs one after another; the remaining tiles' k-blocks are split
+// evenly over rem_pairs pairs, whose partial tiles grad_fixup_kernel adds.
+struct GradWork {
+    int I, J, R;
+    int ni, nj, kblocks, group_i;
+    int npairs, whole, rem, rem_pairs;
+};
+
+struct GradSegment {
+    int tile, kb0, kb1;
+    bool partial;
+    int slot; // of a partial segment: 0 for the first tile of the pair's split range, 1 for the next
+};
+
+// A pair's segments in order; every role walks the same ones.
+struct GradWalk {
+    int next_whole;
+    int64_t u, u1;
+    __device__ __forceinline__ GradWalk(const GradWork &w, int pair)
+    {
+        next_whole = pair;
+        const int64_t U = static_cast<int64_t>(w.rem) * w.kblocks;
+        const bool in = pair < w.rem_pairs;
+        u = in ? pair * U / w.rem_pairs : 0;
+        u1 = in ? (pair + 1) * U / w.rem_pairs : 0;
+        first = static_cast<int>(u / w.kblocks);
+    }
+    int first;
+    __device__ __forceinline__ bool next(const GradWork &w, GradSegment &s)
+    {
+        if (next_whole < w.whole) {
+            s = GradSegment{next_whole, 0, w.kblocks, false, 0};
+            next_whole += w.npairs;
+            return true;
+        }
+        if (u >= u1)
+            return false;
+        const SkSegment sg = sk_segment(u, u1, w.kblocks);
+        const int t = static_cast<int>(sg.t);
+        s = GradSegment{w.whole + t, sg.kb0, sg.kb1, sg.kb1 - sg.kb0 < w.kblocks, t != first};
+        u += sg.kb1 - sg.kb0;
+        return true;
+    }
+};
+
+template <int STAGES, int QSTAGES> struct GradCfg {
+    static constexpr int kABytes = 128 * kGradBR * 2;
+    static constexpr int kBBytes = 128 * kGradBR * 2;
+    static constexpr int kQBytes = 128 * kGradBR;
+    static constexpr int kBOff = STAGES * kABytes;
+    static constexpr int kQOff = kBOff + STAGES * kBBytes;
+    static constexpr int kOutOff = kQOff + QSTAGES * kQBytes; // two 4 KB buffers per epilogue warp
+    static constexpr int kBarOff = kOutOff + 4 * 8192;
+    // full[S], empty[S], qfull[QS], qempty[QS], tfull[2], tempty[2], tensor-memory slot
+    static constexpr int kSmemBytes = kBarOff + (2 * STAGES + 2 * QSTAGES + 4) * 8 + 16 + 1024;
+    static_assert(kSmemBytes <= 232448, "shared memory per CTA");
+    static constexpr int kTmemCols = 512; // two 128 x 256 accumulators per CTA
+};
+
+// 256-row bf16 MMA over the pair (see umma_i8_pair).
+__device__ __forceinline__ void umma_bf16_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                               uint32_t idesc, uint32_t accumulate)
+{
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+// Instruction descriptor of kind::f16 with bf16 A and B and a binary32 D; B is MN-major, A
+// K-major or MN-major.
+__host__ __device__ constexpr uint32_t idesc_bf16(int m, int n, bool a_mn)
+{
+    return (1u << 4)                                // D format: F32
+           | (1u << 7)                              // A format: BF16
+           | (1u << 10)                             // B format: BF16
+           | ((a_mn ? 1u : 0u) << 15)               // A MN-major
+           | (1u << 16)                             // B MN-major
+           | (static_cast<uint32_t>(n >> 3) << 17)  // N / 8
+           | (static_cast<uint32_t>(m >> 4) << 24); // M / 16
+}
+
+// MN-major operand in 128-byte-swizzled shared memory: chunks of 64 values of the M or N side,
+// each [64 k][64 values] with rows of 128 bytes. Eight k rows form a 1024-byte swizzle atom (the
+// stride byte offset); the next chunk starts 8192 bytes on (the leading byte offset). Advancing
+// `saddr` by 2048 selects the next 16 k.
+__device__ __forceinline__ uint64_t sw128_mnmajor_desc(uint32_t saddr)
+{
+    uint64_t d = 0;
+    d |= static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4);
+    d |= static_cast<uint64_t>(8192u >> 4) << 16;
+    d |= static_cast<uint64_t>(1024u >> 4) << 32;
+    d |= static_cast<uint64_t>(1u) << 46;
+    d |= static_cast<uint64_t>(2u) << 61;
+    return d;
+}
+
+// mbar_wait for a barrier that the other CTA of the pair arrives on too: acquire at cluster scope.
+__device__ __forceinline__ bool mbar_wait_cluster(uint32_t bar, uint32_t parity, uint64_t limit_ns)
+{
+    uint64_t t0 = 0;
+    while (true) {
+#pragma unroll 1
+        for (int i = 0; i < 32; ++i) {
+            uint32_t ok;
+            asm volatile("{\n\t.reg .pred p;\n\t"
+                         "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+                         "selp.u32 %0, 1, 0, p;\n\t}"
+                         : "=r"(ok)
+                         : "r"(bar), "r"(parity)
+                         : "memory");
+            if (ok)
+                return true;
+        }
+        const uint64_t now = globaltimer_ns();
+        if (t0 == 0)
+            t0 = now;
+        if (now - t0 > limit_ns) {
+            flag_timeout();
+            return false;
+        }
+    }
+}
+
+// Sixteen codes of one row of Q to bf16(s q), as two 16-byte words.
+// INT8: the byte with its sign bit flipped, u = q + 128, dropped into the bits of 2^15 that
+// weigh 1 .. 128, is the binary32 number 2^15 + u; fma by s minus (2^15 + 128) s leaves s q. Both
+// products are exact when s has 15 significant bits (row_scale), so the only rounding is the one
+// to bf16; rounding s itself is 2^-16 relative, 2^-8 of a bf16 half step.
+// E4M3: exact to f16 in hardware, then to binary32.
+template <bool F8>
+__device__ __forceinline__ void convert16(const uint4 raw, float s, float c, uint4 (&out)[2])
+{
+    const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+    uint32_t o[8];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        float f[4];
+        if constexpr (F8) {
+#pragma unroll
+            for (int p = 0; p < 2; ++p) {
+                uint32_t h;
+                asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\t"
+                    "cvt.rn.f16x2.e4m3x2 %0, lo;\n\t}"
+                    : "=r"(h)
+                    : "r"(p ? w[k] >> 16 : w[k]));
+                asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %2;\n\t"
+                    "cvt.f32.f16 %0, lo;\n\tcvt.f32.f16 %1, hi;\n\t}"
+                    : "=f"(f[2 * p]), "=f"(f[2 * p + 1])
+                    : "r"(h));
+            }
+            const float2 a = mul2(make_float2(f[0], f[1]), splat2(s));
+            const float2 b = mul2(make_float2(f[2], f[3]), splat2(s));
+            o[2 * k] = pack_bf16x2(a.x, a.y);
+            o[2 * k + 1] = pack_bf16x2(b.x, b.y);
+        } else {
+            const uint32_t u = w[k] ^ 0x80808080u;
+            f[0] = __uint_as_float(__byte_perm(u, 0x47000000u, 0x7504));
+            f[1] = __uint_as_float(__byte_perm(u, 0x47000000u, 0x7514));
+            f[2] = __uint_as_float(__byte_perm(u, 0x47000000u, 0x7524));
+            f[3] = __uint_as_float(__byte_perm(u, 0x47000000u, 0x7534));
+            const float2 a = fma2(make_float2(f[0], f[1]), splat2(s), splat2(c));
+            const float2 b = fma2(make_float2(f[2], f[3]), splat2(s), splat2(c));
+            o[2 * k] = pack_bf16x2(a.x, a.y);
+            o[2 * k + 1] = pack_bf16x2(b.x, b.y);
+        }
+    }
+    out[0] = make_uint4(o[0], o[1], o[2], o[3]);
+    out[1] = make_uint4(o[4], o[5], o[6], o[7]);
+}
+
+// The scale as convert16 takes it: to 15 significant bits for INT8 (nearest).
+template <bool F8> __device__ __forceinline__ float row_scale(float s)
+{
+    if constexpr (F8)
+        return s;
+    return __uint_as_float((__float_as_uint(s) + 0x100u) & 0xFFFFFE00u);
+}
+
+// d(silu(g) u): with sig = 1 / (1 + exp(-g)), dg = da u sig (1 + g (1 - sig)), du = da g sig.
+// exp of -|g| only, so nothing overflows; all in binary32.
+__device__ __forceinline__ void silu_grad(float da, float g, float u, float &dg, float &du)
+{
+    const float e = __expf(-fabsf(g));
+    const float inv = __fdividef(1.0f, 1.0f + e);
+    const float small = e * inv;
+    const float sig = g >= 0.0f ? inv : small;
+    const float rest = g >= 0.0f ? small : inv;
+    dg = da * u * (sig * fmaf(g, rest, 1.0f));
+    du = da * (g * sig);
+}
+
+// Eight values of dg and du from eight of da and the stored bf16 gate and up values.
+__device__ __forceinline__ void silu_grad8(const float (&da)[8], const uint4 rg, const uint4 ru,
+                                           uint4 &og, uint4 &ou)
+{
+    float g[8], u[8], a[8], b[8];
+    unpack8(rg, g);
+    unpack8(ru, u);
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        silu_grad(da[i], g[i], u[i], a[i], b[i]);
+    og = make_uint4(pack_bf16x2(a[0], a[1]), pack_bf16x2(a[2], a[3]), pack_bf16x2(a[4], a[5]),
+                    pack_bf16x2(a[6], a[7]));
+    ou = make_uint4(pack_bf16x2(b[0], b[1]), pack_bf16x2(b[2], b[3]), pack_bf16x2(b[4], b[5]),
+                    pack_bf16x2(b[6], b[7]));
+}
+
+// A warp's 32 rows x 128 bytes between global memory and its staging buffer, coalesced; in the
+// buffer, word j of row r is at r * 8 + (j ^ (r & 7)), so a lane's walk along its own row meets no
+// bank conflict. Nothing is read or written outside the valid part.
+__device__ __forceinline__ void stage_load(uint4 *stage, int lane, const char *src, int64_t stride,
+                                           int rows_valid, int bytes_valid)
+{
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const int r = i * 4 + (lane >> 3), j = lane & 7;
+        uint4 x = make_uint4(0u, 0u, 0u, 0u);
+        if (r < rows_valid && j * 16 < bytes_valid)
+            x = ldg_nc_v4(src + r * stride + j * 16);
+        stage[r * 8 + (j ^ (r & 7))] = x;
+    }
+}
+
+__device__ __forceinline__ void stage_store(const uint4 *stage, int lane, char *dst, int64_t stride,
+                                            int rows_valid, int bytes_valid)
+{
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const int r = i * 4 + (lane >> 3), j = lane & 7;
+        if (r < rows_valid && j * 16 < bytes_valid)
+            *reinterpret_cast<uint4 *>(dst + r * stride + j * 16) = stage[r * 8 + (j ^ (r & 7))];
+    }
+}
+
+// A CTA pair per 256 x 256 tile (cta_group::2): each CTA holds 128 rows of A and 128 columns of B
+// and accumulates 128 x 256. WGRAD: A is MN-major. SILU: the epilogue turns C = da into dg and du
+// (out is [I, 2J]) with the forward call's gate|up values.
+template <int STAGES, int QSTAGES, bool WGRAD, bool F8, bool SILU>
+__global__ void __launch_bounds__(kGradThreads, 1)
+    grad_gemm_kernel(const __grid_constant__ CUtensorMap tmA,
+                     const __grid_constant__ CUtensorMap tmQ, const float *__restrict__ scale,
+                     const GradWork w, const uint16_t *__restrict__ gate_up,
+                     uint16_t *__restrict__ out, float *__restrict__ part,
+                     unsigned long long limit_ns)
+{
+    using Cfg = GradCfg<STAGES, QSTAGES>;
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>(
+        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+    const uint32_t sbase = smem_u32(smem);
+    const uint32_t sA = sbase, sB = sbase + Cfg::kBOff, sQ = sbase + Cfg::kQOff;
+    const uint32_t bar_full = sbase + Cfg::kBarOff;       // used in the even CTA
+    const uint32_t bar_empty = bar_full + 8 * STAGES;     // both
+    const uint32_t bar_qfull = bar_empty + 8 * STAGES;    // each CTA its own
+    const uint32_t bar_qempty = bar_qfull + 8 * QSTAGES;
+    const uint32_t bar_tfull = bar_qempty + 8 * QSTAGES;  // both
+    const uint32_t bar_tempty = bar_tfull + 16;           // used in the even CTA
+    const uint32_t tslot = bar_tempty + 16;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_ctarank();
+    const int pair = blockIdx.x >> 1;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < STAGES; ++s) {
+            mbar_init(bar_full + 8 * s, 1 + 2 * kGradConvWarps); // A's bytes, both CTAs' converters
+            mbar_init(bar_empty + 8 * s, 1);
+        }
+        for (int s = 0; s < QSTAGES; ++s) {
+            mbar_init(bar_qfull + 8 * s, 1);
+            mbar_init(bar_qempty + 8 * s, kGradConvWarps);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(bar_tfull + 8 * b, 1);
+            mbar_init(bar_tempty + 8 * b, 8); // 4 epilogue warps in each CTA
+        }
+        fence_mbar_init();
+        tma_prefetch_desc(&tmA);
+        tma_prefetch_desc(&tmQ);
+    }
+    __syncwarp();
+    // both CTAs run, their barriers set, before the pair allocates tensor memory together
+    cluster_sync();
+    if (warp == 1)
+        tmem_alloc_pair(tslot, Cfg::kTmemCols);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem_base =
+        *reinterpret_cast<volatile uint32_t *>(smem + (tslot - sbase));
+
+    if (warp == 0) {
+        if (lane == 0) {
+            pdl_wait();
+            const uint32_t full0 = map_peer_smem(bar_full, 0);
+            uint32_t it = 0;
+            bool ok = true;
+            GradWalk walk(w, pair);
+            GradSegment sg;
+            while (ok && walk.next(w, sg)) {
+                int ib, jb;
+                tile_coords(sg.tile, w.ni, w.nj, w.group_i, ib, jb);
+                const int i0 = ib * kGradTile + static_cast<int>(rank) * 128;
+                for (int kb = sg.kb0; kb < sg.kb1; ++kb, ++it) {
+                    const uint32_t s = it % STAGES;
+                    if (!mbar_wait(bar_empty + 8 * s, ((it / STAGES) & 1u) ^ 1u, limit_ns)) {
+                        ok = false;
+                        break;
+                    }
+                    if (rank == 0)
+                        mbar_expect_tx(bar_full + 8 * s, 2 * Cfg::kABytes);
+                    const uint32_t dst = sA + s * Cfg::kABytes;
+                    if constexpr (WGRAD) {
+                        tma_load_2d_pair(dst, &tmA, full0 + 8 * s, i0, kb * kGradBR);
+                        tma_load_2d_pair(dst + 8192, &tmA, full0 + 8 * s, i0 + 64, kb * kGradBR);
+                    } else {
+                        tma_load_2d_pair(dst, &tmA, full0 + 8 * s, kb * kGradBR, i0);
+                    }
+                }
+            }
+            if (ok) // every stage released by the MMAs before this CTA may leave
+                drain_ring(bar_empty, it, STAGES, limit_ns);
+            pdl_launch_dependents();
+        }
+    } else if (warp == 1) {
+        if (lane == 0 && rank == 0) {
+            constexpr uint32_t idesc = idesc_bf16(kGradTile, kGradTile, WGRAD);
+            uint32_t it = 0, seg = 0;
+            bool ok = true;
+            GradWalk walk(w, pair);
+            GradSegment sg;
+            while (ok && walk.next(w, sg)) {
+                const uint32_t buf = seg & 1u, aph = (seg >> 1) & 1u;
+                ++seg;
+                if (!mbar_wait_cluster(bar_tempty + 8 * buf, aph ^ 1u, limit_ns))
+                    break;
+                tc_fence_after();
+                const uint32_t d = tmem_base + buf * kGradTile;
+                for (int kb = sg.kb0; kb < sg.kb1; ++kb, ++it) {
+                    const uint32_t s = it % STAGES;
+                    if (!mbar_wait_cluster(bar_full + 8 * s, (it / STAGES) & 1u, limit_ns)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint32_t a0 = sA + s * Cfg::kABytes, b0 = sB + s * Cfg::kBBytes;
+#pragma unroll
+                    for (int k = 0; k < kGradBR / 16; ++k)
+                        umma_bf16_pair(d,
+                                       WGRAD ? sw128_mnmajor_desc(a0 + k * 2048)
+                                             : sw128_kmajor_desc(a0 + k * 32),
+                                       sw128_mnmajor_desc(b0 + k * 2048), idesc,
+                                       (kb > sg.kb0 || k > 0) ? 1u : 0u);
+                    umma_commit_pair(bar_empty + 8 * s, 0x3);
+                }
+                if (ok)
+                    umma_commit_pair(bar_tfull + 8 * buf, 0x3);
+            }
+        }
+    } else if (warp < 6) {
+        // epilogue: this CTA's 128 rows of the tile, 32 per warp
+        pdl_wait();
+        const int quarter = warp & 3;
+        uint4 *stage_w = reinterpret_cast<uint4 *>(smem + Cfg::kOutOff) + (warp - 2) * 512;
+        const uint32_t tempty0 = map_peer_smem(bar_tempty, 0);
+        uint32_t seg = 0;
+        GradWalk walk(w, pair);
+        GradSegment sg;
+        while (walk.next(w, sg)) {
+            int ib, jb;
+            tile_coords(sg.tile, w.ni, w.nj, w.group_i, ib, jb);
+            const uint32_t buf = seg & 1u, aph = (seg >> 1) & 1u;
+            ++seg;
+            if (!mbar_wait(bar_tfull + 8 * buf, aph, limit_ns))
+                break;
+            tc_fence_after();
+            const uint32_t tbase =
+                tmem_base + buf * kGradTile + (static_cast<uint32_t>(quarter * 32) << 16);
+            const int row0 = ib * kGradTile + static_cast<int>(rank) * 128 + quarter * 32;
+            const int rows = min(32, w.I - row0); // may be negative: nothing stored
+            if (sg.partial) {
+                float *slot = part + ((static_cast<int64_t>(pair) * 2 + sg.slot) * kGradTile +
+                                      rank * 128 + quarter * 32) * kGradTile;
+#pragma unroll 1
+                for (int c = 0; c < kGradTile / 32; ++c) {
+                    uint32_t r[32];
+                    tmem_ld_32x32b_x32(tbase + c * 32, r);
+                    tmem_ld_wait();
+                    uint4 v[8];
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        v[j] = make_uint4(r[4 * j], r[4 * j + 1], r[4 * j + 2], r[4 * j + 3]);
+                    warp_store_rows(stage_w, v, lane, reinterpret_cast<char *>(slot + c * 32),
+                                    kGradTile * 4, rows, 128);
+                }
+            } else {
+#pragma unroll 1
+                for (int c = 0; c < kGradTile / 64; ++c) {
+                    const int j0 = jb * kGradTile + c * 64;
+                    const int bytes = min(128, (w.J - j0) * 2);
+                    uint32_t r[2][32];
+                    tmem_ld_32x32b_x32(tbase + c * 64, r[0]);
+                    tmem_ld_32x32b_x32(tbase + c * 64 + 32, r[1]);
+                    tmem_ld_wait();
+                    if constexpr (SILU) {
+                        const int64_t ld = static_cast<int64_t>(w.J) * 2;
+                        const char *gu = reinterpret_cast<const char *>(gate_up + row0 * ld + j0);
+                        uint4 *gs = stage_w, *us = stage_w + 256;
+                        stage_load(gs, lane, gu, ld * 2, rows, bytes);
+                        stage_load(us, lane, gu + static_cast<int64_t>(w.J) * 2, ld * 2, rows,
+                                   bytes);
+                        __syncwarp();
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) { // the lane's own row, in place
+                            float da[8];
+#pragma unroll
+                            for (int i = 0; i < 8; ++i)
+                                da[i] = __uint_as_float(r[e >> 2][(e & 3) * 8 + i]);
+                            const int at = lane * 8 + (e ^ (lane & 7));
+                            silu_grad8(da, gs[at], us[at], gs[at], us[at]);
+                        }
+                        __syncwarp();
+                        char *dst = reinterpret_cast<char *>(out + row0 * ld + j0);
+                        stage_store(gs, lane, dst, ld * 2, rows, bytes);
+                        stage_store(us, lane, dst + static_cast<int64_t>(w.J) * 2, ld * 2, rows,
+                                    bytes);
+                        __syncwarp();
+                    } else {
+                        uint4 v[8];
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) {
+                            const uint32_t *f = &r[e >> 2][(e & 3) * 8];
+                            v[e] = make_uint4(
+                                pack_bf16x2(__uint_as_float(f[0]), __uint_as_float(f[1])),
+                                pack_bf16x2(__uint_as_float(f[2]), __uint_as_float(f[3])),
+                                pack_bf16x2(__uint_as_float(f[4]), __uint_as_float(f[5])),
+                                pack_bf16x2(__uint_as_float(f[6]), __uint_as_float(f[7])));
+                        }
+                        warp_store_rows(stage_w, v, lane,
+                                        reinterpret_cast<char *>(out + static_cast<int64_t>(row0) * w.J + j0),
+                                        static_cast<int64_t>(w.J) * 2, rows, bytes);
+                    }
+                }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive_cluster(tempty0 + 8 * buf); // the leader's accumulator is free
+        }
+    } else if (warp == 6) {
+        if (lane == 0) {
+            pdl_wait();
+            uint32_t it = 0;
+            bool ok = true;
+            GradWalk walk(w, pair);
+            GradSegment sg;
+            while (ok && walk.next(w, sg)) {
+                int ib, jb;
+                tile_coords(sg.tile, w.ni, w.nj, w.group_i, ib, jb);
+                const int j0 = jb * kGradTile + static_cast<int>(rank) * 128;
+                for (int kb = sg.kb0; kb < sg.kb1; ++kb, ++it) {
+                    const uint32_t s = it % QSTAGES;
+                    if (!mbar_wait(bar_qempty + 8 * s, ((it / QSTAGES) & 1u) ^ 1u, limit_ns)) {
+                        ok = false;
+                        break;
+                    }
+                    mbar_expect_tx(bar_qfull + 8 * s, Cfg::kQBytes);
+                    tma_load_2d(sQ + s * Cfg::kQBytes, &tmQ, bar_qfull + 8 * s, j0, kb * kGradBR);
+                }
+            }
+            if (ok)
+                drain_ring(bar_qempty, it, QSTAGES, limit_ns);
+        }
+    } else if (warp >= kGradConvWarp0) {
+        // converters: thread t takes the 16-byte piece t % 8 of rows t / 8 and t / 8 + 32 of the
+        // k-block's [64 r][128 j] codes
+        pdl_wait();
+        const int t = threadIdx.x - kGradConvWarp0 * 32;
+        const int piece = t & 7, row = t >> 3;
+        const uint32_t full0 = map_peer_smem(bar_full, 0);
+        // bf16 tile: chunk piece / 4 of 64 columns, row of 128 bytes, 16-byte words swizzled by
+        // the row; lanes of the two chunks store their halves in opposite order, so that eight
+        // lanes of a store fill all banks
+        const uint32_t word = (piece & 3) * 2, swap = piece >> 2;
+        uint32_t dst[2][2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const uint32_t r = row + 32 * h;
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+                dst[h][k] = (piece >> 2) * 8192 + r * 128 + (((word + (k ^ swap)) ^ (r & 7)) << 4);
+        }
+        uint32_t it = 0;
+        bool ok = true;
+        GradWalk walk(w, pair);
+        GradSegment sg;
+        while (ok && walk.next(w, sg)) {
+            for (int kb = sg.kb0; kb < sg.kb1; ++kb, ++it) {
+                float sc[2], cc[2];
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int r = kb * kGradBR + row + 32 * h;
+                    sc[h] = row_scale<F8>(r < w.R ? __ldg(scale + r) : 0.0f);
+                    cc[h] = -32896.0f * sc[h];
+                }
+                const uint32_t qs = it % QSTAGES, s = it % STAGES;
+                if (!mbar_wait(bar_qfull + 8 * qs, (it / QSTAGES) & 1u, limit_ns)) {
+                    ok = false;
+                    break;
+                }
+                uint4 raw[2];
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                    raw[h] = *reinterpret_cast<const uint4 *>(
+                        smem + Cfg::kQOff + qs * Cfg::kQBytes + (row + 32 * h) * 128 + piece * 16);
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(bar_qempty + 8 * qs);
+                uint4 o[2][2];
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                    convert16<F8>(raw[h], sc[h], cc[h], o[h]);
+                if (!mbar_wait(bar_empty + 8 * s, ((it / STAGES) & 1u) ^ 1u, limit_ns)) {
+                    ok = false;
+                    break;
+                }
+                uint8_t *bt = smem + Cfg::kBOff + s * Cfg::kBBytes;
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int k = 0; k < 2; ++k)
+                        *reinterpret_cast<uint4 *>(bt + dst[h][k]) = swap ? o[h][k ^ 1] : o[h][k];
+                fence_proxy_async_smem(); // the tensor cores read what was stored
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive_cluster(full0 + 8 * s);
+            }
+        }
+    }
+    __syncwarp();
+    if (warp == 1)
+        tmem_relinquish_pair();
+    // every MMA, commit and remote arrive is done before either CTA frees its tensor memory
+    tc_fence_before();
+    cluster_sync();
+    tc_fence_after();
+    if (warp == 1)
+        tmem_dealloc_pair(tmem_base, Cfg::kTmemCols);
+}
+
+// Adds the partial tiles of the split tiles, in the order of the pairs, and finishes them: block
+// (x, y) takes 8 rows of remaining tile y.
+template <bool SILU>
+__global__ void __launch_bounds__(256) grad_fixup_kernel(const GradWork w,
+                                                         const float *__restrict__ part,
+                                                         const uint16_t *__restrict__ gate_up,
+                                                         uint16_t *__restrict__ out)
+{
+    if (threadIdx.x == 0)
+        pdl_launch_dependents();
+    pdl_wait();
+    const int t = blockIdx.y;
+    int ib, jb;
+    tile_coords(w.whole + t, w.ni, w.nj, w.group_i, ib, jb);
+    const int rl = blockIdx.x * 8 + (threadIdx.x >> 5);
+    const int row = ib * kGradTile + rl;
+    const int cl = (threadIdx.x & 31) * 8, col = jb * kGradTile + cl;
+    if (row >= w.I || col >= w.J)
+        return;
+    const int64_t U = static_cast<int64_t>(w.rem) * w.kblocks;
+    const int64_t u0 = static_cast<int64_t>(t) * w.kblocks;
+    const int p0 = static_cast<int>(sk_owner_of(u0, U, w.rem_pairs));
+    const int p1 = static_cast<int>(sk_owner_of(u0 + w.kblocks - 1, U, w.rem_pairs));
+    if (p0 == p1)
+        return; // one pair had the whole tile and finished it
+    float f[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        f[i] = 0.0f;
+    for (int p = p0; p <= p1; ++p) {
+        const int64_t begin = p * U / w.rem_pairs;
+        const int slot = static_cast<int>(begin / w.kblocks) != t;
+        const float4 *src = reinterpret_cast<const float4 *>(
+            part + ((static_cast<int64_t>(p) * 2 + slot) * kGradTile + rl) * kGradTile + cl);
+        const float4 a = src[0], b = src[1];
+        f[0] += a.x; f[1] += a.y; f[2] += a.z; f[3] += a.w;
+        f[4] += b.x; f[5] += b.y; f[6] += b.z; f[7] += b.w;
+    }
+    if constexpr (SILU) {
+        const int64_t o = static_cast<int64_t>(row) * 2 * w.J + col;
+        uint4 g = *reinterpret_cast<const uint4 *>(gate_up + o);
+        uint4 u = *reinterpret_cast<const uint4 *>(gate_up + o + w.J);
+        silu_grad8(f, g, u, g, u);
+        *reinterpret_cast<uint4 *>(out + o) = g;
+        *reinterpret_cast<uint4 *>(out + o + w.J) = u;
+    } else {
+        *reinterpret_cast<uint4 *>(out + static_cast<int64_t>(row) * w.J + col) =
+            make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
+                       pack_bf16x2(f[6], f[7]));
+    }
+}
+
+} // namespace w8a8
