@@ -21,6 +21,7 @@ namespace w8a8 {
 constexpr int kGradThreads = 512; // A producer, MMA, 4 epilogue, Q producer, idle, 8 converters
 constexpr int kGradConvWarp0 = 8;
 constexpr int kGradConvWarps = 8;
+constexpr int kGradConvGroups = 4; // groups of converter warps, each on its own k-block
 constexpr int kGradTile = 256; // rows i and columns j of a pair's tile
 constexpr int kGradBR = 64;    // r per k-block: one 128-byte row of bf16
 
@@ -66,6 +67,30 @@ struct GradWalk {
         s = GradSegment{w.whole + t, sg.kb0, sg.kb1, sg.kb1 - sg.kb0 < w.kblocks, t != first};
         u += sg.kb1 - sg.kb0;
         return true;
+    }
+};
+
+// A pair's k-blocks one after another across its segments, some at a time.
+struct GradBlocks {
+    GradWalk walk;
+    GradSegment sg;
+    int kb;
+    bool ok;
+    __device__ __forceinline__ GradBlocks(const GradWork &w, int pair, int skip) : walk(w, pair)
+    {
+        ok = walk.next(w, sg);
+        kb = sg.kb0;
+        if (ok)
+            advance(w, skip);
+    }
+    __device__ __forceinline__ void advance(const GradWork &w, int n)
+    {
+        kb += n;
+        while (ok && kb >= sg.kb1) {
+            const int over = kb - sg.kb1;
+            ok = walk.next(w, sg);
+            kb = sg.kb0 + over;
+        }
     }
 };
 
@@ -291,12 +316,13 @@ __global__ void __launch_bounds__(kGradThreads, 1)
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < STAGES; ++s) {
-            mbar_init(bar_full + 8 * s, 1 + 2 * kGradConvWarps); // A's bytes, both CTAs' converters
+            // A's bytes and the group of converters of each CTA
+            mbar_init(bar_full + 8 * s, 1 + 2 * kGradConvWarps / kGradConvGroups);
             mbar_init(bar_empty + 8 * s, 1);
         }
         for (int s = 0; s < QSTAGES; ++s) {
             mbar_init(bar_qfull + 8 * s, 1);
-            mbar_init(bar_qempty + 8 * s, kGradConvWarps);
+            mbar_init(bar_qempty + 8 * s, kGradConvWarps / kGradConvGroups);
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(bar_tfull + 8 * b, 1);
@@ -500,69 +526,68 @@ __global__ void __launch_bounds__(kGradThreads, 1)
                 drain_ring(bar_qempty, it, QSTAGES, limit_ns);
         }
     } else if (warp >= kGradConvWarp0) {
-        // converters: thread t takes the 16-byte piece t % 8 of rows t / 8 and t / 8 + 32 of the
-        // k-block's [64 r][128 j] codes
+        // converters: group g takes every kGradConvGroups-th k-block, so the waits, loads and
+        // fences of several k-blocks overlap; a thread takes the 16-byte piece t % 8 of rows
+        // t / 8, t / 8 + kStep, ... of the k-block's [64 r][128 j] codes
         pdl_wait();
-        const int t = threadIdx.x - kGradConvWarp0 * 32;
+        constexpr int kGroupThreads = kGradConvWarps / kGradConvGroups * 32;
+        constexpr int kStep = kGroupThreads / 8;
+        constexpr int kRows = kGradBR / kStep;
+        const int ct = threadIdx.x - kGradConvWarp0 * 32;
+        const int group = ct / kGroupThreads, t = ct % kGroupThreads;
         const int piece = t & 7, row = t >> 3;
         const uint32_t full0 = map_peer_smem(bar_full, 0);
         // bf16 tile: chunk piece / 4 of 64 columns, row of 128 bytes, 16-byte words swizzled by
         // the row; lanes of the two chunks store their halves in opposite order, so that eight
         // lanes of a store fill all banks
         const uint32_t word = (piece & 3) * 2, swap = piece >> 2;
-        uint32_t dst[2][2];
+        float next[kRows];
+        auto fetch = [&](int kb) {
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const uint32_t r = row + 32 * h;
-#pragma unroll
-            for (int k = 0; k < 2; ++k)
-                dst[h][k] = (piece >> 2) * 8192 + r * 128 + (((word + (k ^ swap)) ^ (r & 7)) << 4);
-        }
-        uint32_t it = 0;
-        bool ok = true;
-        GradWalk walk(w, pair);
-        GradSegment sg;
-        while (ok && walk.next(w, sg)) {
-            for (int kb = sg.kb0; kb < sg.kb1; ++kb, ++it) {
-                float sc[2], cc[2];
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const int r = kb * kGradBR + row + 32 * h;
-                    sc[h] = row_scale<F8>(r < w.R ? __ldg(scale + r) : 0.0f);
-                    cc[h] = -32896.0f * sc[h];
-                }
-                const uint32_t qs = it % QSTAGES, s = it % STAGES;
-                if (!mbar_wait(bar_qfull + 8 * qs, (it / QSTAGES) & 1u, limit_ns)) {
-                    ok = false;
-                    break;
-                }
-                uint4 raw[2];
-#pragma unroll
-                for (int h = 0; h < 2; ++h)
-                    raw[h] = *reinterpret_cast<const uint4 *>(
-                        smem + Cfg::kQOff + qs * Cfg::kQBytes + (row + 32 * h) * 128 + piece * 16);
-                __syncwarp();
-                if (lane == 0)
-                    mbar_arrive(bar_qempty + 8 * qs);
-                uint4 o[2][2];
-#pragma unroll
-                for (int h = 0; h < 2; ++h)
-                    convert16<F8>(raw[h], sc[h], cc[h], o[h]);
-                if (!mbar_wait(bar_empty + 8 * s, ((it / STAGES) & 1u) ^ 1u, limit_ns)) {
-                    ok = false;
-                    break;
-                }
-                uint8_t *bt = smem + Cfg::kBOff + s * Cfg::kBBytes;
-#pragma unroll
-                for (int h = 0; h < 2; ++h)
-#pragma unroll
-                    for (int k = 0; k < 2; ++k)
-                        *reinterpret_cast<uint4 *>(bt + dst[h][k]) = swap ? o[h][k ^ 1] : o[h][k];
-                fence_proxy_async_smem(); // the tensor cores read what was stored
-                __syncwarp();
-                if (lane == 0)
-                    mbar_arrive_cluster(full0 + 8 * s);
+            for (int h = 0; h < kRows; ++h) {
+                const int r = kb * kGradBR + row + kStep * h;
+                next[h] = r < w.R ? __ldg(scale + r) : 0.0f;
             }
+        };
+        GradBlocks blk(w, pair, group);
+        if (blk.ok)
+            fetch(blk.kb);
+        for (uint32_t it = group; blk.ok; it += kGradConvGroups) {
+            float sc[kRows];
+#pragma unroll
+            for (int h = 0; h < kRows; ++h)
+                sc[h] = row_scale<F8>(next[h]);
+            blk.advance(w, kGradConvGroups);
+            if (blk.ok)
+                fetch(blk.kb); // the next k-block's scales, a k-block early
+            const uint32_t qs = it % QSTAGES, s = it % STAGES;
+            if (!mbar_wait(bar_qfull + 8 * qs, (it / QSTAGES) & 1u, limit_ns))
+                break;
+            uint4 raw[kRows];
+#pragma unroll
+            for (int h = 0; h < kRows; ++h)
+                raw[h] = *reinterpret_cast<const uint4 *>(
+                    smem + Cfg::kQOff + qs * Cfg::kQBytes + (row + kStep * h) * 128 + piece * 16);
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(bar_qempty + 8 * qs);
+            if (!mbar_wait(bar_empty + 8 * s, ((it / STAGES) & 1u) ^ 1u, limit_ns))
+                break;
+            uint8_t *bt = smem + Cfg::kBOff + s * Cfg::kBBytes + (piece >> 2) * 8192;
+#pragma unroll
+            for (int h = 0; h < kRows; ++h) {
+                uint4 o[2];
+                convert16<F8>(raw[h], sc[h], -32896.0f * sc[h], o);
+                const uint32_t r = row + kStep * h;
+                *reinterpret_cast<uint4 *>(bt + r * 128 + (((word + swap) ^ (r & 7)) << 4)) =
+                    swap ? o[1] : o[0];
+                *reinterpret_cast<uint4 *>(bt + r * 128 + (((word + (swap ^ 1)) ^ (r & 7)) << 4)) =
+                    swap ? o[0] : o[1];
+            }
+            fence_proxy_async_smem(); // the tensor cores read what was stored
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive_cluster(full0 + 8 * s);
         }
     }
     __syncwarp();
