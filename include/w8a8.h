@@ -380,7 +380,7 @@ W8A8_API int w8a8_sandwich_rmsnorm_backward(const w8a8_bf16 *dz, const w8a8_bf16
  * block built on it: the step from calibration to tuning a quantized block [W8A8 "The solution:
  * How GPTQ improves on naive quantization" adjusts weights to the rounding error without
  * gradients; gradients are not on the pages]. With wd = bf16(wq s_ch) and xd = bf16(xq s_tok), the
- * dequantized operand rounded once:
+ * dequantized operand rounded once (of a product within 2^-16 relative of the exact one):
  *   w8a8_gemm_dgrad       dx[m,k] = bf16(sum_n dy[m,n] wd[n,k])
  *   w8a8_gemm_wgrad       dw[n,k] = bf16(sum_m dy[m,n] xd[m,k])
  *   w8a8_gemm_dgrad_silu  the down projection's input gradient, continued through
@@ -388,8 +388,7 @@ W8A8_API int w8a8_sandwich_rmsnorm_backward(const w8a8_bf16 *dz, const w8a8_bf16
  *                           da[m,i]         = sum_n dy[m,n] wd[n,i]          (binary32, not stored)
  *                           dgate_up[m,i]   = bf16(da u sig (1 + g (1 - sig))), sig = 1/(1+exp(-g))
  *                           dgate_up[m,I+i] = bf16(da g sig)
- * Sums of bf16 products in binary32 on the tensor cores (kind::f16). INT8 scales enter with 15
- * significant bits (2^-16 relative). A long sum may be split between SMs, its parts added in a
+ * Sums of bf16 products in binary32 on the tensor cores (kind::f16). A long sum may be split between SMs, its parts added in a
  * fixed order: the same call gives the same bits on the same device.
  * dy: bf16 [M,N], the gradient of the linear's output (N of the down projection: the hidden
  * size). wq [N,K] and s_ch fp32 [N]: the forward call's weight; xq [M,K] and s_tok fp32 [M]: its
@@ -397,7 +396,8 @@ W8A8_API int w8a8_sandwich_rmsnorm_backward(const w8a8_bf16 *dz, const w8a8_bf16
  * output ([gate | up] halves, as w8a8_silu_mul_quant reads it); dgate_up likewise. For the gate|up
  * projection itself the rows of wq and the columns of dy only have to agree, so the interleaved
  * weight of w8a8_gemm_silu_quant serves with dy interleaved alike. dx: bf16 [M,K]; dw: bf16 [N,K].
- * Every matrix 16-byte aligned; no output may alias an input. Scales finite, below 2^100.
+ * Every matrix 16-byte aligned; no output may alias an input. Scales finite and at least
+ * 2^-100 or zero; no E4M3 NaN codes.
  * Requires M >= 1, N >= 8, N % 8 == 0, K (I) >= 16, K % 16 == 0, each at most 2^30.
  * workspace: w8a8_gemm_dgrad_workspace_size(M, N, K) bytes (dgrad_silu: K = I), or
  * w8a8_gemm_wgrad_workspace_size(M, N, K), 16-byte aligned, any contents (0: may be NULL).

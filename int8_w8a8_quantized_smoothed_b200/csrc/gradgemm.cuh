@@ -175,59 +175,69 @@ __device__ __forceinline__ bool mbar_wait_cluster(uint32_t bar, uint32_t parity,
     }
 }
 
-// Sixteen codes of one row of Q to bf16(s q), as two 16-byte words.
-// INT8: the byte with its sign bit flipped, u = q + 128, dropped into the bits of 2^15 that
-// weigh 1 .. 128, is the binary32 number 2^15 + u; fma by s minus (2^15 + 128) s leaves s q. Both
-// products are exact when s has 15 significant bits (row_scale), so the only rounding is the one
-// to bf16; rounding s itself is 2^-16 relative, 2^-8 of a bf16 half step.
-// E4M3: exact to f16 in hardware, then to binary32.
-template <bool F8>
-__device__ __forceinline__ void convert16(const uint4 raw, float s, float c, uint4 (&out)[2])
+__device__ __forceinline__ uint32_t sub_bf16x2(uint32_t a, uint32_t b)
 {
-    const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
-    uint32_t o[8];
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-        float f[4];
-        if constexpr (F8) {
-#pragma unroll
-            for (int p = 0; p < 2; ++p) {
-                uint32_t h;
-                asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\t"
-                    "cvt.rn.f16x2.e4m3x2 %0, lo;\n\t}"
-                    : "=r"(h)
-                    : "r"(p ? w[k] >> 16 : w[k]));
-                asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %2;\n\t"
-                    "cvt.f32.f16 %0, lo;\n\tcvt.f32.f16 %1, hi;\n\t}"
-                    : "=f"(f[2 * p]), "=f"(f[2 * p + 1])
-                    : "r"(h));
-            }
-            const float2 a = mul2(make_float2(f[0], f[1]), splat2(s));
-            const float2 b = mul2(make_float2(f[2], f[3]), splat2(s));
-            o[2 * k] = pack_bf16x2(a.x, a.y);
-            o[2 * k + 1] = pack_bf16x2(b.x, b.y);
-        } else {
-            const uint32_t u = w[k] ^ 0x80808080u;
-            f[0] = __uint_as_float(__byte_perm(u, 0x47000000u, 0x7504));
-            f[1] = __uint_as_float(__byte_perm(u, 0x47000000u, 0x7514));
-            f[2] = __uint_as_float(__byte_perm(u, 0x47000000u, 0x7524));
-            f[3] = __uint_as_float(__byte_perm(u, 0x47000000u, 0x7534));
-            const float2 a = fma2(make_float2(f[0], f[1]), splat2(s), splat2(c));
-            const float2 b = fma2(make_float2(f[2], f[3]), splat2(s), splat2(c));
-            o[2 * k] = pack_bf16x2(a.x, a.y);
-            o[2 * k + 1] = pack_bf16x2(b.x, b.y);
-        }
-    }
-    out[0] = make_uint4(o[0], o[1], o[2], o[3]);
-    out[1] = make_uint4(o[4], o[5], o[6], o[7]);
+    uint32_t r;
+    asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
 }
 
-// The scale as convert16 takes it: to 15 significant bits for INT8 (nearest).
-template <bool F8> __device__ __forceinline__ float row_scale(float s)
+__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b)
 {
-    if constexpr (F8)
-        return s;
-    return __uint_as_float((__float_as_uint(s) + 0x100u) & 0xFFFFFE00u);
+    uint32_t r;
+    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+
+__device__ __forceinline__ uint32_t fma_bf16x2(uint32_t a, uint32_t b, uint32_t c)
+{
+    uint32_t r;
+    asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
+    return r;
+}
+
+// A row's scale as the sum of two bf16 values (the nearest one and the nearest to what it leaves,
+// 2^-17 relative together), each in both halves of a word.
+struct RowScale {
+    uint32_t hi, lo;
+};
+
+__device__ __forceinline__ RowScale row_scale(float s)
+{
+    RowScale r;
+    const uint32_t h = __float_as_uint(s) + 0x8000u;
+    r.hi = __byte_perm(h, h, 0x3232);
+    const uint32_t l = __float_as_uint(s - __uint_as_float(h & 0xFFFF0000u)) + 0x8000u;
+    r.lo = __byte_perm(l, l, 0x3232);
+    return r;
+}
+
+// Four codes (one 32-bit word) to bf16(s q), in packed bf16 arithmetic: a conversion instruction
+// (cvt.rn.bf16x2.f32) for each pair held the kernel at 1000 cycles a k-block, its pipe 90% busy.
+// q is exact in bf16, and q hi + bf16(q lo) is rounded once, so the result is bf16 of s q within
+// 2^-16 relative.
+// INT8: the low 7 bits as the fraction of 128 make 128 + (q & 127), the sign bit as the lowest
+// exponent bit of 128 makes 128 or 256; their difference is q.
+// E4M3: exponent and fraction moved to a bf16's places make q 2^-120 (subnormals too).
+template <bool F8>
+__device__ __forceinline__ uint2 convert4(uint32_t w, const RowScale sc)
+{
+    uint32_t v[2];
+    if constexpr (F8) {
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const uint32_t t = __byte_perm(w, 0u, k ? 0x3424 : 0x1404);
+            v[k] = mul_bf16x2(((t >> 4) & 0x07F007F0u) | (t & 0x80008000u), 0x7B807B80u);
+        }
+    } else {
+        const uint32_t m = w & 0x7F7F7F7Fu, n = w & 0x80808080u;
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+            v[k] = sub_bf16x2(__byte_perm(m, 0x43434343u, k ? 0x4342 : 0x4140),
+                              __byte_perm(n, 0x43434343u, k ? 0x4342 : 0x4140));
+    }
+    return make_uint2(fma_bf16x2(v[0], sc.hi, mul_bf16x2(v[0], sc.lo)),
+                      fma_bf16x2(v[1], sc.hi, mul_bf16x2(v[1], sc.lo)));
 }
 
 // d(silu(g) u): with sig = 1 / (1 + exp(-g)), dg = da u sig (1 + g (1 - sig)), du = da g sig.
@@ -526,63 +536,53 @@ __global__ void __launch_bounds__(kGradThreads, 1)
                 drain_ring(bar_qempty, it, QSTAGES, limit_ns);
         }
     } else if (warp >= kGradConvWarp0) {
-        // converters: group g takes every kGradConvGroups-th k-block, so the waits, loads and
-        // fences of several k-blocks overlap; a thread takes the 16-byte piece t % 8 of rows
-        // t / 8, t / 8 + kStep, ... of the k-block's [64 r][128 j] codes
+        // converters: group g (two warps) takes every kGradConvGroups-th k-block, so the waits,
+        // loads and fences of several k-blocks overlap. A thread takes one row r of the k-block's
+        // [64 r][128 j] codes, eight 16-byte pieces starting at its own lane's, so that eight
+        // lanes of a load, or of a store into the swizzled bf16 tile, fill all banks.
         pdl_wait();
-        constexpr int kGroupThreads = kGradConvWarps / kGradConvGroups * 32;
-        constexpr int kStep = kGroupThreads / 8;
-        constexpr int kRows = kGradBR / kStep;
+        static_assert(kGradConvWarps * 32 == kGradConvGroups * kGradBR, "a thread per row");
         const int ct = threadIdx.x - kGradConvWarp0 * 32;
-        const int group = ct / kGroupThreads, t = ct % kGroupThreads;
-        const int piece = t & 7, row = t >> 3;
+        const int group = ct / kGradBR, row = ct % kGradBR;
         const uint32_t full0 = map_peer_smem(bar_full, 0);
-        // bf16 tile: chunk piece / 4 of 64 columns, row of 128 bytes, 16-byte words swizzled by
-        // the row; lanes of the two chunks store their halves in opposite order, so that eight
-        // lanes of a store fill all banks
-        const uint32_t word = (piece & 3) * 2, swap = piece >> 2;
-        float next[kRows];
+        float next = 0.0f;
         auto fetch = [&](int kb) {
-#pragma unroll
-            for (int h = 0; h < kRows; ++h) {
-                const int r = kb * kGradBR + row + kStep * h;
-                next[h] = r < w.R ? __ldg(scale + r) : 0.0f;
-            }
+            const int r = kb * kGradBR + row;
+            next = r < w.R ? __ldg(scale + r) : 0.0f;
         };
         GradBlocks blk(w, pair, group);
         if (blk.ok)
             fetch(blk.kb);
         for (uint32_t it = group; blk.ok; it += kGradConvGroups) {
-            float sc[kRows];
-#pragma unroll
-            for (int h = 0; h < kRows; ++h)
-                sc[h] = row_scale<F8>(next[h]);
+            const RowScale sc = row_scale(next);
             blk.advance(w, kGradConvGroups);
             if (blk.ok)
-                fetch(blk.kb); // the next k-block's scales, a k-block early
+                fetch(blk.kb); // the next k-block's scale, a k-block early
             const uint32_t qs = it % QSTAGES, s = it % STAGES;
             if (!mbar_wait(bar_qfull + 8 * qs, (it / QSTAGES) & 1u, limit_ns))
                 break;
-            uint4 raw[kRows];
+            const uint8_t *src = smem + Cfg::kQOff + qs * Cfg::kQBytes + row * 128;
+            uint4 raw[8];
 #pragma unroll
-            for (int h = 0; h < kRows; ++h)
-                raw[h] = *reinterpret_cast<const uint4 *>(
-                    smem + Cfg::kQOff + qs * Cfg::kQBytes + (row + kStep * h) * 128 + piece * 16);
+            for (int k = 0; k < 8; ++k)
+                raw[k] = *reinterpret_cast<const uint4 *>(src + (((k + lane) & 7) << 4));
             __syncwarp();
             if (lane == 0)
                 mbar_arrive(bar_qempty + 8 * qs);
             if (!mbar_wait(bar_empty + 8 * s, ((it / STAGES) & 1u) ^ 1u, limit_ns))
                 break;
-            uint8_t *bt = smem + Cfg::kBOff + s * Cfg::kBBytes + (piece >> 2) * 8192;
+            uint8_t *bt = smem + Cfg::kBOff + s * Cfg::kBBytes + row * 128;
 #pragma unroll
-            for (int h = 0; h < kRows; ++h) {
-                uint4 o[2];
-                convert16<F8>(raw[h], sc[h], -32896.0f * sc[h], o);
-                const uint32_t r = row + kStep * h;
-                *reinterpret_cast<uint4 *>(bt + r * 128 + (((word + swap) ^ (r & 7)) << 4)) =
-                    swap ? o[1] : o[0];
-                *reinterpret_cast<uint4 *>(bt + r * 128 + (((word + (swap ^ 1)) ^ (r & 7)) << 4)) =
-                    swap ? o[0] : o[1];
+            for (int k = 0; k < 8; ++k) {
+                const uint32_t piece = (k + lane) & 7; // columns 16 piece .. 16 piece + 15
+                uint8_t *chunk = bt + (piece >> 2) * 8192;
+                const uint32_t word = (piece & 3) * 2;
+                const uint2 a = convert4<F8>(raw[k].x, sc), b = convert4<F8>(raw[k].y, sc);
+                const uint2 c = convert4<F8>(raw[k].z, sc), d = convert4<F8>(raw[k].w, sc);
+                *reinterpret_cast<uint4 *>(chunk + ((word ^ (row & 7)) << 4)) =
+                    make_uint4(a.x, a.y, b.x, b.y);
+                *reinterpret_cast<uint4 *>(chunk + (((word + 1) ^ (row & 7)) << 4)) =
+                    make_uint4(c.x, c.y, d.x, d.y);
             }
             fence_proxy_async_smem(); // the tensor cores read what was stored
             __syncwarp();

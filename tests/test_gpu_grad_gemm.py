@@ -1,9 +1,8 @@
 """The gradients of a W8A8 linear and of the gated feed-forward block against their formulas in
 binary64.
 
-The dequantized operand bf16(s q) is reproduced exactly (one binary32 product, then bf16; INT8
-scales to 15 significant bits), so the only differences are the tensor cores' binary32 additions
-and the output's rounding. A k = 16 instruction adds its sixteen exact products to the accumulator
+The dequantized operand is reproduced exactly (the scale as two bf16 parts, bf16(q hi + bf16(q
+lo))), so the only differences are the tensor cores' binary32 additions and the output's rounding. A k = 16 instruction adds its sixteen exact products to the accumulator
 with an error of at most one unit in the last place of the largest partial sum, 2^-23 of
 sum |products|; over R terms R / 16 + 1 instructions, and up to 74 parts of a split sum."""
 import numpy as np
@@ -33,12 +32,23 @@ def _codes(shape, f8, seed):
     return x.cuda().to(w8.FP8)
 
 
+def _bf16_part(s):
+    """The nearest bf16 (halves away from zero) of positive binary32 values."""
+    return ((s.view(torch.int32) + 0x8000) & ~0xFFFF).view(torch.float32)
+
+
+def _round_bf16(x):
+    """Binary64 values rounded to eight significant bits, ties to even, in one step."""
+    m, e = torch.frexp(x)
+    return torch.ldexp(torch.round(m * 256), e - 8)
+
+
 def _dequantized(q, s):
-    """bf16(s q) as the kernels form it, in binary64."""
-    if q.dtype == torch.int8:
-        bits = (s.view(torch.int32) + 0x100) & ~0x1FF
-        s = bits.view(torch.float32)
-    return (q.float() * s[:, None]).bfloat16().double()
+    """The bf16 operand s q as the kernels form it, in binary64: q hi + bf16(q lo), rounded."""
+    hi = _bf16_part(s)
+    lo = _bf16_part((s - hi).abs()) * torch.sign(s - hi)
+    v = q.float().double()
+    return _round_bf16(v * hi.double()[:, None] + _round_bf16(v * lo.double()[:, None]))
 
 
 def _dy(M, N, seed):
@@ -127,12 +137,12 @@ def test_gated_block_backward(M, N, K, f8):
 
 
 def test_against_the_unrounded_definition():
-    """The operand's own rounding included: at most 2^-8 + 2^-16 of each product."""
+    """The operand's own rounding included: at most 2^-8 of each product, and 2^-15 before it."""
     M, N, K = 200, 1024, 512
     dy, q, s = _dy(M, N, 11), _codes((N, K), False, 12), _scales(N, 13)
     b = q.double() * s.double()[:, None]
     ref, mag = dy.double() @ b, dy.double().abs() @ b.abs()
-    tol = _tol(ref, mag, N) + (2.0 ** -8 + 2.0 ** -16) * mag
+    tol = _tol(ref, mag, N) + (2.0 ** -8 + 2.0 ** -15) * mag
     _assert_close(w8.w8a8_gemm_dgrad(dy, q, s), ref, tol)
 
 
@@ -147,6 +157,12 @@ def test_extreme_codes_and_zero_scales():
     got = w8.w8a8_gemm_dgrad(dy, q, s)
     assert torch.equal(got[0].float(), torch.arange(-128, 128, device="cuda") * 0.5)
     assert not got[1].any()
+    # every finite E4M3 value, subnormals among them, times a power of two
+    codes = torch.arange(256, device="cuda").to(torch.uint8)
+    codes[codes & 0x7F == 0x7F] = 0  # NaN
+    q8 = codes.view(w8.FP8).repeat(N, 1).contiguous()
+    got = w8.w8a8_gemm_dgrad_fp8(dy, q8, s)
+    assert torch.equal(got[0].float(), codes.view(w8.FP8).float() * 0.5)
 
 
 @pytest.mark.parametrize("name,M,N,K", [("dgrad", 40, 4096, 512), ("wgrad", 2100, 264, 272),
