@@ -177,7 +177,7 @@ int launch_sandwich_back_gate(const SandwichBack &a, int gate_kind, const Sandwi
 
 // ------------------------------------------------------------------ gradients of a W8A8 linear
 
-constexpr int kGradStages = 5, kGradQStages = 4;
+constexpr int kGradStages = 5, kGradQStages = 6;
 // A pair takes at least this many k-blocks of a split tile: below it the partial tile's store and
 // the addition cost more than the k-blocks.
 constexpr int64_t kGradMinSplit = 8;

@@ -18,9 +18,9 @@
 
 namespace w8a8 {
 
-constexpr int kGradThreads = 512; // A producer, MMA, 4 epilogue, Q producer, idle, 8 converters
+constexpr int kGradThreads = 768; // A producer, MMA, Q producer, idle; 4 epilogue; 16 converters
 constexpr int kGradConvWarp0 = 8;
-constexpr int kGradConvWarps = 8;
+constexpr int kGradConvWarps = 16;
 constexpr int kGradConvGroups = 4; // groups of converter warps, each on its own k-block
 constexpr int kGradTile = 256; // rows i and columns j of a pair's tile
 constexpr int kGradBR = 64;    // r per k-block: one 128-byte row of bf16
@@ -100,8 +100,8 @@ template <int STAGES, int QSTAGES> struct GradCfg {
     static constexpr int kQBytes = 128 * kGradBR;
     static constexpr int kBOff = STAGES * kABytes;
     static constexpr int kQOff = kBOff + STAGES * kBBytes;
-    static constexpr int kOutOff = kQOff + QSTAGES * kQBytes; // two 4 KB buffers per epilogue warp
-    static constexpr int kBarOff = kOutOff + 4 * 8192;
+    static constexpr int kOutOff = kQOff + QSTAGES * kQBytes; // 4 KB per epilogue warp
+    static constexpr int kBarOff = kOutOff + 4 * 4096;
     // full[S], empty[S], qfull[QS], qempty[QS], tfull[2], tempty[2], tensor-memory slot
     static constexpr int kSmemBytes = kBarOff + (2 * STAGES + 2 * QSTAGES + 4) * 8 + 16 + 1024;
     static_assert(kSmemBytes <= 232448, "shared memory per CTA");
@@ -269,30 +269,37 @@ __device__ __forceinline__ void silu_grad8(const float (&da)[8], const uint4 rg,
                     pack_bf16x2(b[6], b[7]));
 }
 
-// A warp's 32 rows x 128 bytes between global memory and its staging buffer, coalesced; in the
-// buffer, word j of row r is at r * 8 + (j ^ (r & 7)), so a lane's walk along its own row meets no
-// bank conflict. Nothing is read or written outside the valid part.
+// A warp's 32 rows of ROW 16-byte words between global memory and its staging buffer, coalesced;
+// word j of row r is kept at r * ROW + (j ^ (r * ROW / 8 & (ROW - 1))), so a lane's walk along its
+// own row meets no bank conflict. Nothing is read or written outside the valid part.
+template <int ROW> __device__ __forceinline__ int stage_at(int r, int j)
+{
+    return r * ROW + (j ^ ((r * ROW >> 3) & (ROW - 1)));
+}
+
+template <int ROW>
 __device__ __forceinline__ void stage_load(uint4 *stage, int lane, const char *src, int64_t stride,
                                            int rows_valid, int bytes_valid)
 {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const int r = i * 4 + (lane >> 3), j = lane & 7;
+    for (int i = 0; i < ROW; ++i) {
+        const int r = (i * 32 + lane) / ROW, j = lane % ROW;
         uint4 x = make_uint4(0u, 0u, 0u, 0u);
         if (r < rows_valid && j * 16 < bytes_valid)
             x = ldg_nc_v4(src + r * stride + j * 16);
-        stage[r * 8 + (j ^ (r & 7))] = x;
+        stage[stage_at<ROW>(r, j)] = x;
     }
 }
 
+template <int ROW>
 __device__ __forceinline__ void stage_store(const uint4 *stage, int lane, char *dst, int64_t stride,
                                             int rows_valid, int bytes_valid)
 {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const int r = i * 4 + (lane >> 3), j = lane & 7;
+    for (int i = 0; i < ROW; ++i) {
+        const int r = (i * 32 + lane) / ROW, j = lane % ROW;
         if (r < rows_valid && j * 16 < bytes_valid)
-            *reinterpret_cast<uint4 *>(dst + r * stride + j * 16) = stage[r * 8 + (j ^ (r & 7))];
+            *reinterpret_cast<uint4 *>(dst + r * stride + j * 16) = stage[stage_at<ROW>(r, j)];
     }
 }
 
@@ -421,11 +428,11 @@ __global__ void __launch_bounds__(kGradThreads, 1)
                     umma_commit_pair(bar_tfull + 8 * buf, 0x3);
             }
         }
-    } else if (warp < 6) {
+    } else if (warp >= 4 && warp < 8) {
         // epilogue: this CTA's 128 rows of the tile, 32 per warp
         pdl_wait();
         const int quarter = warp & 3;
-        uint4 *stage_w = reinterpret_cast<uint4 *>(smem + Cfg::kOutOff) + (warp - 2) * 512;
+        uint4 *stage_w = reinterpret_cast<uint4 *>(smem + Cfg::kOutOff) + quarter * 256;
         const uint32_t tempty0 = map_peer_smem(bar_tempty, 0);
         uint32_t seg = 0;
         GradWalk walk(w, pair);
@@ -442,76 +449,74 @@ __global__ void __launch_bounds__(kGradThreads, 1)
                 tmem_base + buf * kGradTile + (static_cast<uint32_t>(quarter * 32) << 16);
             const int row0 = ib * kGradTile + static_cast<int>(rank) * 128 + quarter * 32;
             const int rows = min(32, w.I - row0); // may be negative: nothing stored
-            if (sg.partial) {
-                float *slot = part + ((static_cast<int64_t>(pair) * 2 + sg.slot) * kGradTile +
-                                      rank * 128 + quarter * 32) * kGradTile;
+            const int64_t ld = static_cast<int64_t>(w.J) * (SILU ? 4 : 2); // bytes
+            float *slot = part + ((static_cast<int64_t>(pair) * 2 + sg.slot) * kGradTile +
+                                  rank * 128 + quarter * 32) * kGradTile;
 #pragma unroll 1
-                for (int c = 0; c < kGradTile / 32; ++c) {
-                    uint32_t r[32];
-                    tmem_ld_32x32b_x32(tbase + c * 32, r);
-                    tmem_ld_wait();
-                    uint4 v[8];
-#pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        v[j] = make_uint4(r[4 * j], r[4 * j + 1], r[4 * j + 2], r[4 * j + 3]);
-                    warp_store_rows(stage_w, v, lane, reinterpret_cast<char *>(slot + c * 32),
-                                    kGradTile * 4, rows, 128);
-                }
-            } else {
-#pragma unroll 1
-                for (int c = 0; c < kGradTile / 64; ++c) {
-                    const int j0 = jb * kGradTile + c * 64;
-                    const int bytes = min(128, (w.J - j0) * 2);
-                    uint32_t r[2][32];
-                    tmem_ld_32x32b_x32(tbase + c * 64, r[0]);
-                    tmem_ld_32x32b_x32(tbase + c * 64 + 32, r[1]);
-                    tmem_ld_wait();
-                    if constexpr (SILU) {
-                        const int64_t ld = static_cast<int64_t>(w.J) * 2;
-                        const char *gu = reinterpret_cast<const char *>(gate_up + row0 * ld + j0);
-                        uint4 *gs = stage_w, *us = stage_w + 256;
-                        stage_load(gs, lane, gu, ld * 2, rows, bytes);
-                        stage_load(us, lane, gu + static_cast<int64_t>(w.J) * 2, ld * 2, rows,
-                                   bytes);
-                        __syncwarp();
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) { // the lane's own row, in place
-                            float da[8];
-#pragma unroll
-                            for (int i = 0; i < 8; ++i)
-                                da[i] = __uint_as_float(r[e >> 2][(e & 3) * 8 + i]);
-                            const int at = lane * 8 + (e ^ (lane & 7));
-                            silu_grad8(da, gs[at], us[at], gs[at], us[at]);
-                        }
-                        __syncwarp();
-                        char *dst = reinterpret_cast<char *>(out + row0 * ld + j0);
-                        stage_store(gs, lane, dst, ld * 2, rows, bytes);
-                        stage_store(us, lane, dst + static_cast<int64_t>(w.J) * 2, ld * 2, rows,
-                                    bytes);
-                        __syncwarp();
-                    } else {
-                        uint4 v[8];
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) {
-                            const uint32_t *f = &r[e >> 2][(e & 3) * 8];
-                            v[e] = make_uint4(
-                                pack_bf16x2(__uint_as_float(f[0]), __uint_as_float(f[1])),
-                                pack_bf16x2(__uint_as_float(f[2]), __uint_as_float(f[3])),
-                                pack_bf16x2(__uint_as_float(f[4]), __uint_as_float(f[5])),
-                                pack_bf16x2(__uint_as_float(f[6]), __uint_as_float(f[7])));
-                        }
-                        warp_store_rows(stage_w, v, lane,
-                                        reinterpret_cast<char *>(out + static_cast<int64_t>(row0) * w.J + j0),
-                                        static_cast<int64_t>(w.J) * 2, rows, bytes);
+            for (int c = 0; c < kGradTile / 32; ++c) {
+                const int j0 = jb * kGradTile + c * 32;
+                uint32_t r[32];
+                if constexpr (SILU) {
+                    if (!sg.partial) {
+                        const char *gu = reinterpret_cast<const char *>(gate_up) + row0 * ld + j0 * 2;
+                        const int bytes = min(64, (w.J - j0) * 2);
+                        stage_load<4>(stage_w, lane, gu, ld, rows, bytes);
+                        stage_load<4>(stage_w + 128, lane, gu + static_cast<int64_t>(w.J) * 2, ld,
+                                      rows, bytes);
                     }
                 }
+                tmem_ld_32x32b_x32(tbase + c * 32, r);
+                tmem_ld_wait();
+                if (sg.partial) {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        stage_w[stage_at<8>(lane, j)] =
+                            make_uint4(r[4 * j], r[4 * j + 1], r[4 * j + 2], r[4 * j + 3]);
+                    __syncwarp();
+                    stage_store<8>(stage_w, lane, reinterpret_cast<char *>(slot + c * 32),
+                                   kGradTile * 4, rows, 128);
+                } else if constexpr (SILU) {
+                    __syncwarp();
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) { // the lane's own row, in place
+                        float da[8];
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            da[i] = __uint_as_float(r[e * 8 + i]);
+                        uint4 *g = stage_w + stage_at<4>(lane, e);
+                        silu_grad8(da, g[0], g[128], g[0], g[128]);
+                    }
+                    __syncwarp();
+                    char *dst = reinterpret_cast<char *>(out) + row0 * ld + j0 * 2;
+                    const int bytes = min(64, (w.J - j0) * 2);
+                    stage_store<4>(stage_w, lane, dst, ld, rows, bytes);
+                    stage_store<4>(stage_w + 128, lane, dst + static_cast<int64_t>(w.J) * 2, ld,
+                                   rows, bytes);
+                } else { // two chunks of columns go out together, 128 bytes a row
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const uint32_t *f = &r[e * 8];
+                        stage_w[stage_at<8>(lane, (c & 1) * 4 + e)] = make_uint4(
+                            pack_bf16x2(__uint_as_float(f[0]), __uint_as_float(f[1])),
+                            pack_bf16x2(__uint_as_float(f[2]), __uint_as_float(f[3])),
+                            pack_bf16x2(__uint_as_float(f[4]), __uint_as_float(f[5])),
+                            pack_bf16x2(__uint_as_float(f[6]), __uint_as_float(f[7])));
+                    }
+                    if (c & 1) {
+                        __syncwarp();
+                        stage_store<8>(stage_w, lane,
+                                       reinterpret_cast<char *>(out) + row0 * ld + (j0 - 32) * 2, ld,
+                                       rows, min(128, (w.J - j0 + 32) * 2));
+                    }
+                }
+                __syncwarp();
             }
             tc_fence_before();
             __syncwarp();
             if (lane == 0)
                 mbar_arrive_cluster(tempty0 + 8 * buf); // the leader's accumulator is free
         }
-    } else if (warp == 6) {
+    } else if (warp == 2) {
         if (lane == 0) {
             pdl_wait();
             uint32_t it = 0;
@@ -536,14 +541,17 @@ __global__ void __launch_bounds__(kGradThreads, 1)
                 drain_ring(bar_qempty, it, QSTAGES, limit_ns);
         }
     } else if (warp >= kGradConvWarp0) {
-        // converters: group g (two warps) takes every kGradConvGroups-th k-block, so the waits,
-        // loads and fences of several k-blocks overlap. A thread takes one row r of the k-block's
-        // [64 r][128 j] codes, eight 16-byte pieces starting at its own lane's, so that eight
-        // lanes of a load, or of a store into the swizzled bf16 tile, fill all banks.
+        // converters: group g (four warps) takes every kGradConvGroups-th k-block, so the waits,
+        // loads and fences of several k-blocks overlap. Two threads share a row r of the
+        // k-block's [64 r][128 j] codes, every other 16-byte piece each, starting at the lane's
+        // own, so that eight lanes of a load, or of a store into the swizzled bf16 tile, fill all
+        // banks.
         pdl_wait();
-        static_assert(kGradConvWarps * 32 == kGradConvGroups * kGradBR, "a thread per row");
+        constexpr int kGroupThreads = 2 * kGradBR;
+        static_assert(kGradConvWarps * 32 == kGradConvGroups * kGroupThreads, "two threads a row");
         const int ct = threadIdx.x - kGradConvWarp0 * 32;
-        const int group = ct / kGradBR, row = ct % kGradBR;
+        const int group = ct / kGroupThreads;
+        const int row = ct % kGradBR, half = ct / kGradBR & 1;
         const uint32_t full0 = map_peer_smem(bar_full, 0);
         float next = 0.0f;
         auto fetch = [&](int kb) {
@@ -555,17 +563,14 @@ __global__ void __launch_bounds__(kGradThreads, 1)
             fetch(blk.kb);
         for (uint32_t it = group; blk.ok; it += kGradConvGroups) {
             const RowScale sc = row_scale(next);
-            blk.advance(w, kGradConvGroups);
-            if (blk.ok)
-                fetch(blk.kb); // the next k-block's scale, a k-block early
             const uint32_t qs = it % QSTAGES, s = it % STAGES;
             if (!mbar_wait(bar_qfull + 8 * qs, (it / QSTAGES) & 1u, limit_ns))
                 break;
             const uint8_t *src = smem + Cfg::kQOff + qs * Cfg::kQBytes + row * 128;
-            uint4 raw[8];
+            uint4 raw[4];
 #pragma unroll
-            for (int k = 0; k < 8; ++k)
-                raw[k] = *reinterpret_cast<const uint4 *>(src + (((k + lane) & 7) << 4));
+            for (int k = 0; k < 4; ++k)
+                raw[k] = *reinterpret_cast<const uint4 *>(src + (((2 * k + half + lane) & 7) << 4));
             __syncwarp();
             if (lane == 0)
                 mbar_arrive(bar_qempty + 8 * qs);
@@ -573,8 +578,8 @@ __global__ void __launch_bounds__(kGradThreads, 1)
                 break;
             uint8_t *bt = smem + Cfg::kBOff + s * Cfg::kBBytes + row * 128;
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                const uint32_t piece = (k + lane) & 7; // columns 16 piece .. 16 piece + 15
+            for (int k = 0; k < 4; ++k) {
+                const uint32_t piece = (2 * k + half + lane) & 7; // columns 16 piece .. + 15
                 uint8_t *chunk = bt + (piece >> 2) * 8192;
                 const uint32_t word = (piece & 3) * 2;
                 const uint2 a = convert4<F8>(raw[k].x, sc), b = convert4<F8>(raw[k].y, sc);
@@ -588,6 +593,10 @@ __global__ void __launch_bounds__(kGradThreads, 1)
             __syncwarp();
             if (lane == 0)
                 mbar_arrive_cluster(full0 + 8 * s);
+            // the scale of the group's next k-block, after the fence, which would wait for it
+            blk.advance(w, kGradConvGroups);
+            if (blk.ok)
+                fetch(blk.kb);
         }
     }
     __syncwarp();
