@@ -9,8 +9,8 @@ package does not need a GPU, but every compute call does.
     q, s = w8a8_smooth_rmsnorm_quant(x, gamma_smoothed, eps)
     y = w8a8_gemm_dequant(q, s, wq, s_ch)
 """
-import contextlib
 import ctypes as C
+import functools
 import os
 import threading
 
@@ -165,43 +165,61 @@ def _need(t, name, dtype, shape=None):
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
 
 
-_HERE = contextlib.nullcontext()
+def _arg(t, name, dtype, shape, index):
+    """The address of a tensor that has this type, shape (None: any) and device and is contiguous;
+    raises as _need does otherwise. None stays None."""
+    if t is None:
+        return None
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and (shape is None or t.shape == shape)
+            and t.is_contiguous() and t.get_device() == index):
+        _need(t, name, dtype, shape)
+        raise ValueError(f"{name} is on {t.device}, expected cuda:{index}")
+    return t.data_ptr()
 
 
-def _place(x, stream):
-    """The context a call runs in: x's device current, and the given stream (default: the current
-    stream of x's device), so that outputs and workspaces allocated inside belong to the stream
+def _matrix(t, name, dtype):
+    """(rows, columns, device index) of the tensor that a call takes its sizes from."""
+    _need(t, name, dtype)
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be two-dimensional, got {tuple(t.shape)}")
+    return (*t.shape, t.get_device())
+
+
+def _on_device(fn):
+    """Runs a call with its first tensor's device current and on the given stream (default: that
+    device's current stream), so that outputs and workspaces allocated inside belong to the stream
     that uses them."""
-    if stream is None:
-        if x.device.index == torch.cuda.current_device():
-            return _HERE
-        stream = torch.cuda.current_stream(x.device)
-    elif stream.device != x.device:
-        raise ValueError(f"stream is on {stream.device}, the tensors on {x.device}")
-    return torch.cuda.stream(stream)
+    @functools.wraps(fn)
+    def call(x, *args, stream=None, **kw):
+        if stream is None:
+            if not x.is_cuda or x.get_device() == torch.cuda.current_device():
+                return fn(x, *args, **kw)
+            stream = torch.cuda.current_stream(x.device)
+        elif stream.device != x.device:
+            raise ValueError(f"stream is on {stream.device}, the tensors on {x.device}")
+        with torch.cuda.stream(stream):
+            return fn(x, *args, **kw)
+    return call
 
 
-def _same_device(x, **tensors):
-    for name, t in tensors.items():
-        if t is not None and t.device != x.device:
-            raise ValueError(f"{name} is on {t.device}, expected {x.device}")
-
-
-def _scratch(workspace, nbytes, device):
-    """(pointer, size) of the caller's workspace, or of a new one for this call alone (nothing is
-    kept between calls that use it, so calls on any streams and captured graphs cannot share it).
-    The last element keeps it alive."""
+def _scratch(workspace, nbytes, index):
+    """(address, size, the tensor) of the caller's workspace, or of a new one for this call alone:
+    nothing is kept between calls, so calls on any streams and captured graphs cannot share it."""
     if workspace is None:
-        workspace = torch.empty(nbytes, dtype=torch.uint8, device=device) if nbytes else None
-    elif isinstance(workspace, Workspace):
+        if nbytes == 0:
+            return None, 0, None
+        workspace = torch.empty(nbytes, dtype=torch.uint8, device=index)
+        return workspace.data_ptr(), nbytes, workspace
+    if isinstance(workspace, Workspace):
         workspace, _ = workspace.get(nbytes)
-    else:
-        _need(workspace, "workspace", workspace.dtype)
-        if workspace.device != device:
-            raise ValueError(f"workspace is on {workspace.device}, expected {device}")
-    if workspace is None:
-        return None, 0, None
-    return _ptr(workspace), workspace.numel() * workspace.element_size(), workspace
+        if workspace is None:
+            return None, 0, None
+    ptr = _arg(workspace, "workspace", workspace.dtype, None, index)
+    return ptr, workspace.numel() * workspace.element_size(), workspace
+
+
+def _current_stream(index):
+    return torch._C._cuda_getCurrentRawStream(index)
 
 
 def w8a8_status_string(status: int) -> str:
@@ -749,111 +767,101 @@ def w8a8_block_decode(x, attn, gamma1, sinv_o, gamma2, qkv, o, gate_up_il, down,
 _GATE_NONE, _GATE_TOKEN, _GATE_CHANNEL, _GATE_FULL = 0, 1, 2, 3
 
 
-def _gate_kind(gate, M, K):
+def _gate_arg(gate, M, K, index):
+    """(kind, address) of a gate: its kind follows from its shape and type."""
     if gate is None:
-        return _GATE_NONE
+        return _GATE_NONE, None
     if not isinstance(gate, torch.Tensor):
         raise TypeError("gate must be a torch.Tensor")
-    shape = tuple(gate.shape)
     for kind, dtype, want in ((_GATE_TOKEN, torch.float32, (M, 1)),
                               (_GATE_CHANNEL, torch.float32, (1, K)),
                               (_GATE_FULL, torch.bfloat16, (M, K))):
-        if shape == want and gate.dtype == dtype:
-            _need(gate, "gate", dtype)
-            return kind
+        if gate.shape == want and gate.dtype is dtype:
+            return kind, _arg(gate, "gate", dtype, want, index)
     raise ValueError(f"gate must be fp32 ({M}, 1), fp32 (1, {K}) or bf16 ({M}, {K}), got "
-                     f"{gate.dtype} {shape}")
+                     f"{gate.dtype} {tuple(gate.shape)}")
 
 
 def _sandwich_quant(name, code, y, residual, gamma_smoothed, eps, gamma_post, eps_post, gate,
-                    res_scale, h_out, q, s_tok, stream):
-    _need(y, "y", torch.bfloat16)
-    if y.dim() != 2:
-        raise ValueError(f"y must be [M, K], got {tuple(y.shape)}")
-    M, K = y.shape
-    _need(residual, "residual", torch.bfloat16, (M, K))
-    _need(gamma_smoothed, "gamma_smoothed", torch.float32, (K,))
-    if gamma_post is not None:
-        _need(gamma_post, "gamma_post", torch.float32, (K,))
-    kind = _gate_kind(gate, M, K)
-    with _place(y, stream):
-        h_out = torch.empty_like(y) if h_out is None else h_out
-        q = torch.empty((M, K), dtype=code, device=y.device) if q is None else q
-        s_tok = torch.empty(M, dtype=torch.float32, device=y.device) if s_tok is None else s_tok
-        _need(h_out, "h_out", torch.bfloat16, (M, K))
-        _need(q, "q", code, (M, K))
-        _need(s_tok, "s_tok", torch.float32, (M,))
-        _same_device(y, residual=residual, gamma_smoothed=gamma_smoothed, gamma_post=gamma_post,
-                     gate=gate, h_out=h_out, q=q, s_tok=s_tok)
-        _check(name, getattr(lib(), name)(
-            _ptr(y), _ptr(residual), _ptr(gamma_post), float(eps if eps_post is None else eps_post),
-            _ptr(gate), kind, float(res_scale), _ptr(gamma_smoothed), float(eps), M, K,
-            _ptr(h_out), _ptr(q), _ptr(s_tok), _stream(None)))
+                    res_scale, h_out, q, s_tok):
+    M, K, index = _matrix(y, "y", torch.bfloat16)
+    if residual is None or gamma_smoothed is None:
+        raise TypeError("residual and gamma_smoothed must be torch.Tensors")
+    kind, pgate = _gate_arg(gate, M, K, index)
+    h_out = torch.empty_like(y) if h_out is None else h_out
+    q = torch.empty((M, K), dtype=code, device=index) if q is None else q
+    s_tok = torch.empty(M, dtype=torch.float32, device=index) if s_tok is None else s_tok
+    rc = getattr(lib(), name)(
+        y.data_ptr(), _arg(residual, "residual", torch.bfloat16, (M, K), index),
+        _arg(gamma_post, "gamma_post", torch.float32, (K,), index),
+        eps if eps_post is None else eps_post, pgate, kind, res_scale,
+        _arg(gamma_smoothed, "gamma_smoothed", torch.float32, (K,), index), eps, M, K,
+        _arg(h_out, "h_out", torch.bfloat16, (M, K), index), _arg(q, "q", code, (M, K), index),
+        _arg(s_tok, "s_tok", torch.float32, (M,), index), _current_stream(index))
+    if rc:
+        raise W8A8Error(name, rc)
     return q, s_tok, h_out
 
 
+@_on_device
 def w8a8_sandwich_rmsnorm_quant(y, residual, gamma_smoothed, eps, gamma_post=None, eps_post=None,
-                                gate=None, res_scale=1.0, h_out=None, q=None, s_tok=None,
-                                stream=None):
+                                gate=None, res_scale=1.0, h_out=None, q=None, s_tok=None):
     """The step between two blocks: h = bf16(res_scale * residual + gate * n), with n the RMSNorm
     of the block's output y by gamma_post (n = y without gamma_post), then the next block's
     smoothed RMSNorm of h with per-token int8 codes. gate: None, fp32 [M, 1] (per token), fp32
     [1, K] (per channel) or bf16 [M, K]. eps_post defaults to eps. h_out may be residual (in
-    place). Returns (q, s_tok, h)."""
+    place). stream: by keyword, default the current one. Returns (q, s_tok, h)."""
     return _sandwich_quant("w8a8_sandwich_rmsnorm_quant", torch.int8, y, residual, gamma_smoothed,
-                           eps, gamma_post, eps_post, gate, res_scale, h_out, q, s_tok, stream)
+                           eps, gamma_post, eps_post, gate, res_scale, h_out, q, s_tok)
 
 
+@_on_device
 def w8a8_sandwich_rmsnorm_quant_fp8(y, residual, gamma_smoothed, eps, gamma_post=None,
                                     eps_post=None, gate=None, res_scale=1.0, h_out=None, q=None,
-                                    s_tok=None, stream=None):
+                                    s_tok=None):
     """w8a8_sandwich_rmsnorm_quant with FP8 (E4M3) codes."""
     return _sandwich_quant("w8a8_sandwich_rmsnorm_quant_fp8", FP8, y, residual, gamma_smoothed,
-                           eps, gamma_post, eps_post, gate, res_scale, h_out, q, s_tok, stream)
+                           eps, gamma_post, eps_post, gate, res_scale, h_out, q, s_tok)
 
 
 def w8a8_sandwich_rmsnorm_backward_workspace_size(M: int, K: int) -> int:
     return int(lib().w8a8_sandwich_rmsnorm_backward_workspace_size(M, K))
 
 
+@_on_device
 def w8a8_sandwich_rmsnorm_backward(dz, y, h, gamma_smoothed, eps, dh=None, gamma_post=None,
                                    eps_post=None, gate=None, res_scale=1.0, dy=None,
-                                   dresidual=None, workspace=None, stream=None):
+                                   dresidual=None, workspace=None):
     """The backward pass of w8a8_sandwich_rmsnorm_quant (either code), the quantization passed
     straight through: dz bf16 [M, K] is the gradient of the codes' values, dh bf16 [M, K] (or
     None) the gradient that reaches h by the residual stream, y and h the forward call's input
-    and stored output. dresidual may be dh (in place). Returns (dy, dresidual, dgamma_smoothed,
-    dgamma_post or None, dgate or None), dgate in gate's shape and type."""
-    _need(dz, "dz", torch.bfloat16)
-    if dz.dim() != 2:
-        raise ValueError(f"dz must be [M, K], got {tuple(dz.shape)}")
-    M, K = dz.shape
-    _need(y, "y", torch.bfloat16, (M, K))
-    _need(h, "h", torch.bfloat16, (M, K))
-    if dh is not None:
-        _need(dh, "dh", torch.bfloat16, (M, K))
-    _need(gamma_smoothed, "gamma_smoothed", torch.float32, (K,))
-    if gamma_post is not None:
-        _need(gamma_post, "gamma_post", torch.float32, (K,))
-    kind = _gate_kind(gate, M, K)
-    with _place(dz, stream):
-        dy = torch.empty_like(dz) if dy is None else dy
-        dresidual = torch.empty_like(dz) if dresidual is None else dresidual
-        _need(dy, "dy", torch.bfloat16, (M, K))
-        _need(dresidual, "dresidual", torch.bfloat16, (M, K))
-        _same_device(dz, y=y, h=h, dh=dh, gamma_smoothed=gamma_smoothed, gamma_post=gamma_post,
-                     gate=gate, dy=dy, dresidual=dresidual)
-        dpre = torch.empty_like(gamma_smoothed)
-        dpost = None if gamma_post is None else torch.empty_like(gamma_post)
-        dgate = None if gate is None else torch.empty_like(gate)
-        wptr, wbytes, keep = _scratch(workspace, w8a8_sandwich_rmsnorm_backward_workspace_size(M, K),
-                                      dz.device)
-        _check("w8a8_sandwich_rmsnorm_backward", lib().w8a8_sandwich_rmsnorm_backward(
-            _ptr(dz), _ptr(dh), _ptr(y), _ptr(h), _ptr(gamma_post),
-            float(eps if eps_post is None else eps_post), _ptr(gate), kind, float(res_scale),
-            _ptr(gamma_smoothed), float(eps), M, K, _ptr(dy), _ptr(dresidual), _ptr(dpost),
-            _ptr(dgate), _ptr(dpre), wptr, wbytes, _stream(None)))
-        del keep
+    and stored output. dresidual may be dh (in place). stream: by keyword, default the current
+    one. Returns (dy, dresidual, dgamma_smoothed, dgamma_post or None, dgate or None), dgate in
+    gate's shape and type."""
+    M, K, index = _matrix(dz, "dz", torch.bfloat16)
+    if y is None or h is None or gamma_smoothed is None:
+        raise TypeError("y, h and gamma_smoothed must be torch.Tensors")
+    kind, pgate = _gate_arg(gate, M, K, index)
+    L = lib()
+    dy = torch.empty_like(dz) if dy is None else dy
+    dresidual = torch.empty_like(dz) if dresidual is None else dresidual
+    dpre = torch.empty(K, dtype=torch.float32, device=index)
+    dpost = None if gamma_post is None else torch.empty(K, dtype=torch.float32, device=index)
+    dgate = None if gate is None else torch.empty_like(gate)
+    wptr, wbytes, keep = _scratch(
+        workspace, L.w8a8_sandwich_rmsnorm_backward_workspace_size(M, K), index)
+    rc = L.w8a8_sandwich_rmsnorm_backward(
+        dz.data_ptr(), _arg(dh, "dh", torch.bfloat16, (M, K), index),
+        _arg(y, "y", torch.bfloat16, (M, K), index), _arg(h, "h", torch.bfloat16, (M, K), index),
+        _arg(gamma_post, "gamma_post", torch.float32, (K,), index),
+        eps if eps_post is None else eps_post, pgate, kind, res_scale,
+        _arg(gamma_smoothed, "gamma_smoothed", torch.float32, (K,), index), eps, M, K,
+        _arg(dy, "dy", torch.bfloat16, (M, K), index),
+        _arg(dresidual, "dresidual", torch.bfloat16, (M, K), index),
+        None if dpost is None else dpost.data_ptr(), None if dgate is None else dgate.data_ptr(),
+        dpre.data_ptr(), wptr, wbytes, _current_stream(index))
+    if rc:
+        raise W8A8Error("w8a8_sandwich_rmsnorm_backward", rc)
     return dy, dresidual, dpre, dpost, dgate
 
 
@@ -865,73 +873,79 @@ def w8a8_gemm_wgrad_workspace_size(M: int, N: int, K: int) -> int:
     return int(lib().w8a8_gemm_wgrad_workspace_size(M, N, K))
 
 
-def _grad(name, code, dy, q, scale, rows, out, out_name, gate_up, workspace, stream):
+def _grad(name, code, dy, q, scale, rows, out, out_name, gate_up, workspace):
     """rows: which of dy's dimensions the code matrix q has as its rows (1: N, the weight; 0: M,
     the activations)."""
-    _need(dy, "dy", torch.bfloat16)
-    if dy.dim() != 2:
-        raise ValueError(f"dy must be [M, N], got {tuple(dy.shape)}")
-    M, N = dy.shape
+    M, N, index = _matrix(dy, "dy", torch.bfloat16)
+    R = N if rows else M
     qn, sn = ("wq", "s_ch") if rows else ("xq", "s_tok")
-    _need(q, qn, code)
-    if q.dim() != 2 or q.shape[0] != dy.shape[rows]:
-        raise ValueError(f"{qn} must be [{dy.shape[rows]}, K] for dy {tuple(dy.shape)}, got "
-                         f"{tuple(q.shape)}")
+    pq = _arg(q, qn, code, None, index)
+    if pq is None or scale is None:
+        raise TypeError(f"{qn} and {sn} must be torch.Tensors")
+    if q.dim() != 2 or q.shape[0] != R:
+        raise ValueError(f"{qn} must be [{R}, K] for dy ({M}, {N}), got {tuple(q.shape)}")
     K = q.shape[1]
-    _need(scale, sn, torch.float32, (dy.shape[rows],))
+    ps = _arg(scale, sn, torch.float32, (R,), index)
     shape = (M, K) if rows else (N, K)
+    extra = ()
     if gate_up is not None:
         shape = (M, 2 * K)
-        _need(gate_up, "gate_up", torch.bfloat16, shape)
-    with _place(dy, stream):
-        out = torch.empty(shape, dtype=torch.bfloat16, device=dy.device) if out is None else out
-        _need(out, out_name, torch.bfloat16, shape)
-        _same_device(dy, **{qn: q, sn: scale, "gate_up": gate_up, out_name: out})
-        size = w8a8_gemm_dgrad_workspace_size if rows else w8a8_gemm_wgrad_workspace_size
-        wptr, wbytes, keep = _scratch(workspace, size(M, N, K), dy.device)
-        extra = () if gate_up is None else (_ptr(gate_up),)
-        _check(name, getattr(lib(), name)(_ptr(dy), _ptr(q), _ptr(scale), M, N, K, *extra,
-                                          _ptr(out), wptr, wbytes, _stream(None)))
-        del keep
+        extra = (_arg(gate_up, "gate_up", torch.bfloat16, shape, index),)
+    L = lib()
+    out = torch.empty(shape, dtype=torch.bfloat16, device=index) if out is None else out
+    size = L.w8a8_gemm_dgrad_workspace_size if rows else L.w8a8_gemm_wgrad_workspace_size
+    wptr, wbytes, keep = _scratch(workspace, size(M, N, K), index)
+    rc = getattr(L, name)(dy.data_ptr(), pq, ps, M, N, K, *extra,
+                          _arg(out, out_name, torch.bfloat16, shape, index), wptr, wbytes,
+                          _current_stream(index))
+    if rc:
+        raise W8A8Error(name, rc)
     return out
 
 
-def w8a8_gemm_dgrad(dy, wq, s_ch, dx=None, workspace=None, stream=None):
+@_on_device
+def w8a8_gemm_dgrad(dy, wq, s_ch, dx=None, workspace=None):
     """Input gradient of a W8A8 linear: dx [M, K] = dy [M, N] @ (wq * s_ch[:, None]) in bf16, the
-    weight's int8 codes dequantized inside the kernel."""
-    return _grad("w8a8_gemm_dgrad", torch.int8, dy, wq, s_ch, 1, dx, "dx", None, workspace, stream)
+    weight's int8 codes dequantized by the library. stream: by keyword, default the current one."""
+    return _grad("w8a8_gemm_dgrad", torch.int8, dy, wq, s_ch, 1, dx, "dx", None, workspace)
 
 
-def w8a8_gemm_dgrad_fp8(dy, wq, s_ch, dx=None, workspace=None, stream=None):
+@_on_device
+def w8a8_gemm_dgrad_fp8(dy, wq, s_ch, dx=None, workspace=None):
     """w8a8_gemm_dgrad with FP8 (E4M3) weight codes."""
-    return _grad("w8a8_gemm_dgrad_fp8", FP8, dy, wq, s_ch, 1, dx, "dx", None, workspace, stream)
+    return _grad("w8a8_gemm_dgrad_fp8", FP8, dy, wq, s_ch, 1, dx, "dx", None, workspace)
 
 
-def w8a8_gemm_dgrad_silu(dy, wq, s_ch, gate_up, dgate_up=None, workspace=None, stream=None):
+@_on_device
+def w8a8_gemm_dgrad_silu(dy, wq, s_ch, gate_up, dgate_up=None, workspace=None):
     """The gated feed-forward block's backward step: da = dy [M, H] @ (wq * s_ch[:, None]) with the
     down projection's wq [H, I], then the gradients of silu(gate) * up from the forward gate|up
-    values gate_up [M, 2I]. Returns dgate_up [M, 2I]; da is not stored."""
+    values gate_up [M, 2I]. stream: by keyword, default the current one. Returns dgate_up [M, 2I];
+    da is not stored."""
     if gate_up is None:
         raise TypeError("gate_up must be a torch.Tensor")
     return _grad("w8a8_gemm_dgrad_silu", torch.int8, dy, wq, s_ch, 1, dgate_up, "dgate_up",
-                 gate_up, workspace, stream)
+                 gate_up, workspace)
 
 
-def w8a8_gemm_dgrad_silu_fp8(dy, wq, s_ch, gate_up, dgate_up=None, workspace=None, stream=None):
+@_on_device
+def w8a8_gemm_dgrad_silu_fp8(dy, wq, s_ch, gate_up, dgate_up=None, workspace=None):
     """w8a8_gemm_dgrad_silu with FP8 (E4M3) weight codes."""
     if gate_up is None:
         raise TypeError("gate_up must be a torch.Tensor")
     return _grad("w8a8_gemm_dgrad_silu_fp8", FP8, dy, wq, s_ch, 1, dgate_up, "dgate_up", gate_up,
-                 workspace, stream)
+                 workspace)
 
 
-def w8a8_gemm_wgrad(dy, xq, s_tok, dw=None, workspace=None, stream=None):
+@_on_device
+def w8a8_gemm_wgrad(dy, xq, s_tok, dw=None, workspace=None):
     """Weight gradient of a W8A8 linear, passed straight through the weight's rounding: dw [N, K] =
-    dy [M, N]^T @ (xq * s_tok[:, None]) in bf16, the activations' int8 codes dequantized inside
-    the kernel."""
-    return _grad("w8a8_gemm_wgrad", torch.int8, dy, xq, s_tok, 0, dw, "dw", None, workspace, stream)
+    dy [M, N]^T @ (xq * s_tok[:, None]) in bf16, the activations' int8 codes dequantized by the
+    library. stream: by keyword, default the current one."""
+    return _grad("w8a8_gemm_wgrad", torch.int8, dy, xq, s_tok, 0, dw, "dw", None, workspace)
 
 
-def w8a8_gemm_wgrad_fp8(dy, xq, s_tok, dw=None, workspace=None, stream=None):
+@_on_device
+def w8a8_gemm_wgrad_fp8(dy, xq, s_tok, dw=None, workspace=None):
     """w8a8_gemm_wgrad with FP8 (E4M3) activation codes."""
-    return _grad("w8a8_gemm_wgrad_fp8", FP8, dy, xq, s_tok, 0, dw, "dw", None, workspace, stream)
+    return _grad("w8a8_gemm_wgrad_fp8", FP8, dy, xq, s_tok, 0, dw, "dw", None, workspace)

@@ -132,4 +132,4 @@ def test_binding_checks():
         w8.w8a8_sandwich_rmsnorm_backward(y, y, y, torch.ones(64), 1e-5)
     for gate in (torch.ones(64), torch.ones(4, 64), torch.ones(4, 1, dtype=torch.bfloat16)):
         with pytest.raises(ValueError, match="gate must be"):
-            w8._gate_kind(gate, 4, 64)
+            w8._gate_arg(gate, 4, 64, 0)
