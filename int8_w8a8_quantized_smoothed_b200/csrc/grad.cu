@@ -177,11 +177,6 @@ int launch_sandwich_back_gate(const SandwichBack &a, int gate_kind, const Sandwi
 
 // ------------------------------------------------------------------ gradients of a W8A8 linear
 
-constexpr int kGradStages = 5, kGradQStages = 6;
-// A pair takes at least this many k-blocks of a split tile: below it the partial tile's store and
-// the addition cost more than the k-blocks.
-constexpr int64_t kGradMinSplit = 8;
-
 int check_grad_shape(int64_t M, int64_t N, int64_t K)
 {
     if (M < 1 || N < 8 || K < 16)
@@ -191,13 +186,27 @@ int check_grad_shape(int64_t M, int64_t N, int64_t K)
     return W8A8_OK;
 }
 
+struct GradPlan {
+    GradWork w;
+    bool conv;          // the GEMM converts Q itself; otherwise Q goes through a bf16 workspace
+    size_t part_off;    // partial tiles of a split, after the bf16 operand
+    size_t ws_bytes;
+};
+
+// From this many rows i on, Q is converted once ahead of the product. The kernel that converts
+// its tiles itself does each of them again for every 256 rows and runs at about 1.1 PFLOP/s, the
+// other at about 1.5, after a pass over Q of 3 bytes a code.
+constexpr int64_t kGradDequantRows = 1024;
+
 // False when there are more tiles than an int counts.
-bool grad_work(int64_t I, int64_t J, int64_t R, int sms, GradWork *w)
+bool grad_plan(int64_t I, int64_t J, int64_t R, int sms, GradPlan *p)
 {
     const int64_t ni = (I + kGradTile - 1) / kGradTile, nj = (J + kGradTile - 1) / kGradTile;
     const int64_t tiles = ni * nj, kb = (R + kGradBR - 1) / kGradBR, pairs = sms / 2;
     if (tiles > (1 << 30))
         return false;
+    GradWork *w = &p->w;
+    p->conv = I < kGradDequantRows;
     w->I = static_cast<int>(I);
     w->J = static_cast<int>(J);
     w->R = static_cast<int>(R);
@@ -208,16 +217,22 @@ bool grad_work(int64_t I, int64_t J, int64_t R, int sms, GradWork *w)
     w->npairs = static_cast<int>(pairs);
     w->whole = static_cast<int>(tiles / pairs * pairs);
     w->rem = static_cast<int>(tiles % pairs);
-    w->rem_pairs = static_cast<int>(
-        w->rem == 0 ? 0 : std::min(pairs, std::max<int64_t>(w->rem, w->rem * kb / kGradMinSplit)));
+    w->rem_pairs = w->rem;
+    if (w->rem > 0) {
+        // The last tiles' k-blocks are split over all pairs where that saves more time than the
+        // partial tiles cost: a k-block takes 0.55 us (converted here) or 0.35 us; the second
+        // launch about 4 us, storing and adding partial tiles up to 8 us (by their rows).
+        const int64_t split = std::min(pairs, std::max<int64_t>(w->rem, w->rem * kb / 4));
+        const double each = p->conv ? 0.55 : 0.35;
+        const double saved = each * (kb - static_cast<double>(w->rem * kb) / split);
+        if (saved > 4.0 + 8.0 * std::min<int64_t>(I, kGradTile) / kGradTile)
+            w->rem_pairs = static_cast<int>(split);
+    }
+    p->part_off = p->conv ? 0 : (static_cast<size_t>(R) * static_cast<size_t>(J) * 2 + 255) / 256 * 256;
+    p->ws_bytes = p->part_off;
+    if (w->rem_pairs > w->rem)
+        p->ws_bytes += static_cast<size_t>(w->rem_pairs) * 2 * kGradTile * kGradTile * sizeof(float);
     return true;
-}
-
-size_t grad_ws_bytes(const GradWork &w)
-{
-    return w.rem_pairs > w.rem
-               ? static_cast<size_t>(w.rem_pairs) * 2 * kGradTile * kGradTile * sizeof(float)
-               : 0;
 }
 
 // 2-D row-major tensor, `inner` elements of `esize` bytes per row, 128-byte boxes.
@@ -237,18 +252,19 @@ int encode_grad(CUtensorMap *map, const void *base, int64_t rows, int64_t inner,
     return r == CUDA_SUCCESS ? W8A8_OK : W8A8_ERR_CUDA;
 }
 
-template <bool WGRAD, bool F8, bool SILU>
+template <bool CONV, bool WGRAD, bool F8, bool SILU>
 int launch_grad(const CUtensorMap &ta, const CUtensorMap &tq, const float *scale,
                 const GradWork &w, const uint16_t *gate_up, uint16_t *out, float *part, int dev,
                 cudaStream_t st)
 {
-    using Cfg = GradCfg<kGradStages, kGradQStages>;
-    auto kernel = grad_gemm_kernel<kGradStages, kGradQStages, WGRAD, F8, SILU>;
+    using Cfg = GradCfg<CONV>;
+    auto kernel = grad_gemm_kernel<CONV, WGRAD, F8, SILU>;
     if (int rc = ensure_smem(reinterpret_cast<const void *>(kernel), dev, Cfg::kSmemBytes))
         return rc;
     const unsigned pairs = static_cast<unsigned>(w.whole > 0 ? w.npairs : w.rem_pairs);
-    if (int rc = launch_kernel_cluster(kernel, dim3(2 * pairs), dim3(kGradThreads), Cfg::kSmemBytes,
-                                       st, 2u, ta, tq, scale, w, gate_up, out, part, kWaitLimitNs))
+    if (int rc = launch_kernel_cluster(kernel, dim3(2 * pairs), dim3(Cfg::kThreads),
+                                       Cfg::kSmemBytes, st, 2u, ta, tq, scale, w, gate_up, out,
+                                       part, kWaitLimitNs))
         return rc;
     if (w.rem_pairs <= w.rem)
         return W8A8_OK; // no tile was split
@@ -258,6 +274,20 @@ int launch_grad(const CUtensorMap &ta, const CUtensorMap &tq, const float *scale
     const unsigned rows = static_cast<unsigned>(std::min(w.I, kGradTile));
     return launch_kernel(grad_fixup_kernel<SILU>, dim3((rows + 7) / 8, static_cast<unsigned>(w.rem)),
                          dim3(256), 0, st, w, static_cast<const float *>(part), gate_up, out);
+}
+
+template <bool F8>
+int launch_dequant(const void *q, const float *scale, int64_t R, int64_t J, uint16_t *out, int dev,
+                   int sms, cudaStream_t st)
+{
+    const void *fn = reinterpret_cast<const void *>(&grad_dequant_kernel<F8>);
+    if (int rc = ensure_smem(fn, dev, 0))
+        return rc;
+    const int64_t nvec = R * (J / 16);
+    const int64_t grid = std::min<int64_t>((nvec + 255) / 256, static_cast<int64_t>(sms) * 8);
+    return launch_kernel(grad_dequant_kernel<F8>, dim3(static_cast<unsigned>(grid)), dim3(256), 0,
+                         st, static_cast<const uint8_t *>(q), scale, nvec,
+                         static_cast<uint32_t>(J / 16), out);
 }
 
 // dy [M, N]; Q: wq [N, K] (input gradient) or xq [M, K] (weight gradient).
@@ -279,19 +309,32 @@ int grad_impl(bool f8, const uint16_t *dy, const void *q, const float *scale, in
     int dev, sms;
     if ((rc = current_device(&dev, &sms)))
         return rc;
-    GradWork w;
-    if (!grad_work(WGRAD ? N : M, K, WGRAD ? M : N, sms, &w))
+    const int64_t R = WGRAD ? M : N;
+    GradPlan p;
+    if (!grad_plan(WGRAD ? N : M, K, R, sms, &p))
         return W8A8_ERR_UNSUPPORTED_SHAPE;
-    if (grad_ws_bytes(w) > 0 && (workspace == nullptr || workspace_bytes < grad_ws_bytes(w)))
+    if (p.ws_bytes > 0 && (workspace == nullptr || workspace_bytes < p.ws_bytes))
         return W8A8_ERR_WORKSPACE;
-    CUtensorMap ta, tq;
-    if (encode_grad(&ta, dy, M, N, 2, WGRAD ? kGradBR : 128, true) ||
-        encode_grad(&tq, q, WGRAD ? M : N, K, 1, kGradBR, false))
-        return W8A8_ERR_CUDA;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    float *part = static_cast<float *>(workspace);
-    return f8 ? launch_grad<WGRAD, true, SILU>(ta, tq, scale, w, gate_up, out, part, dev, st)
-              : launch_grad<WGRAD, false, SILU>(ta, tq, scale, w, gate_up, out, part, dev, st);
+    float *part = reinterpret_cast<float *>(static_cast<char *>(workspace) + p.part_off);
+    CUtensorMap ta, tq;
+    if (encode_grad(&ta, dy, M, N, 2, WGRAD ? kGradBR : 128, true))
+        return W8A8_ERR_CUDA;
+    if (p.conv) {
+        if (encode_grad(&tq, q, R, K, 1, kGradBR, false))
+            return W8A8_ERR_CUDA;
+        return f8 ? launch_grad<true, WGRAD, true, SILU>(ta, tq, scale, p.w, gate_up, out, part,
+                                                         dev, st)
+                  : launch_grad<true, WGRAD, false, SILU>(ta, tq, scale, p.w, gate_up, out, part,
+                                                          dev, st);
+    }
+    uint16_t *b = static_cast<uint16_t *>(workspace);
+    if (encode_grad(&tq, b, R, K, 2, kGradBR, true))
+        return W8A8_ERR_CUDA;
+    if ((rc = f8 ? launch_dequant<true>(q, scale, R, K, b, dev, sms, st)
+                 : launch_dequant<false>(q, scale, R, K, b, dev, sms, st)))
+        return rc;
+    return launch_grad<false, WGRAD, false, SILU>(ta, tq, scale, p.w, gate_up, out, part, dev, st);
 }
 
 size_t grad_workspace(int64_t M, int64_t N, int64_t K, bool wgrad)
@@ -301,8 +344,8 @@ size_t grad_workspace(int64_t M, int64_t N, int64_t K, bool wgrad)
     int dev, sms = 148;
     if (current_device(&dev, &sms))
         sms = 148;
-    GradWork w;
-    return grad_work(wgrad ? N : M, K, wgrad ? M : N, sms, &w) ? grad_ws_bytes(w) : 0;
+    GradPlan p;
+    return grad_plan(wgrad ? N : M, K, wgrad ? M : N, sms, &p) ? p.ws_bytes : 0;
 }
 
 } // namespace

@@ -7,11 +7,14 @@
 //   weight gradient  i = output channel, r = token,   j = input channel:  A = dy^T, Q = xq, s = s_tok
 //
 // Both sum over the rows of the 8-bit matrix Q, which is the dimension its scales belong to, so
-// the scale cannot wait for the epilogue: warps of the kernel turn Q's tiles into scaled bf16
-// tiles in shared memory (a weight is read from HBM as one byte and never stored as two). The
-// codes are exact in bf16; the product with the scale is rounded once. B's tiles keep Q's layout
-// (rows r, j contiguous: the MMA's MN-major form), as does A in the weight gradient (dy's rows
-// are r), so nothing is transposed in memory.
+// the scale cannot wait for the epilogue: Q becomes a scaled bf16 operand, its codes exact in bf16
+// and the product with the scale rounded once. Two forms:
+//   CONV      warps of the kernel turn Q's tiles into bf16 tiles in shared memory (a code is read
+//             from HBM as one byte and never stored as two), for few rows i;
+//   otherwise grad_dequant_kernel writes all of B first and the kernel loads both operands: each
+//             of Q's tiles is converted once, not once for every tile of rows i.
+// B's tiles keep Q's layout (rows r, j contiguous: the MMA's MN-major form), as does A in the
+// weight gradient (dy's rows are r), so nothing is transposed in memory.
 #pragma once
 
 #include "gemm.cuh"
@@ -94,7 +97,11 @@ struct GradBlocks {
     }
 };
 
-template <int STAGES, int QSTAGES> struct GradCfg {
+// CONV: the kernel converts Q itself; otherwise B is a bf16 matrix loaded like A.
+template <bool CONV> struct GradCfg {
+    static constexpr int STAGES = CONV ? 5 : 6;
+    static constexpr int QSTAGES = CONV ? 6 : 0;
+    static constexpr int kThreads = CONV ? kGradThreads : 256; // without: no converter warps
     static constexpr int kABytes = 128 * kGradBR * 2;
     static constexpr int kBBytes = 128 * kGradBR * 2;
     static constexpr int kQBytes = 128 * kGradBR;
@@ -103,7 +110,7 @@ template <int STAGES, int QSTAGES> struct GradCfg {
     static constexpr int kOutOff = kQOff + QSTAGES * kQBytes; // 4 KB per epilogue warp
     static constexpr int kBarOff = kOutOff + 4 * 4096;
     // full[S], empty[S], qfull[QS], qempty[QS], tfull[2], tempty[2], tensor-memory slot
-    static constexpr int kSmemBytes = kBarOff + (2 * STAGES + 2 * QSTAGES + 4) * 8 + 16 + 1024;
+    static constexpr int kSmemBytes = kBarOff + (2 * STAGES + 2 * QSTAGES + 6) * 8 + 16 + 1024;
     static_assert(kSmemBytes <= 232448, "shared memory per CTA");
     static constexpr int kTmemCols = 512; // two 128 x 256 accumulators per CTA
 };
@@ -306,15 +313,16 @@ __device__ __forceinline__ void stage_store(const uint4 *stage, int lane, char *
 // A CTA pair per 256 x 256 tile (cta_group::2): each CTA holds 128 rows of A and 128 columns of B
 // and accumulates 128 x 256. WGRAD: A is MN-major. SILU: the epilogue turns C = da into dg and du
 // (out is [I, 2J]) with the forward call's gate|up values.
-template <int STAGES, int QSTAGES, bool WGRAD, bool F8, bool SILU>
-__global__ void __launch_bounds__(kGradThreads, 1)
+template <bool CONV, bool WGRAD, bool F8, bool SILU>
+__global__ void __launch_bounds__(GradCfg<CONV>::kThreads, 1)
     grad_gemm_kernel(const __grid_constant__ CUtensorMap tmA,
                      const __grid_constant__ CUtensorMap tmQ, const float *__restrict__ scale,
                      const GradWork w, const uint16_t *__restrict__ gate_up,
                      uint16_t *__restrict__ out, float *__restrict__ part,
                      unsigned long long limit_ns)
 {
-    using Cfg = GradCfg<STAGES, QSTAGES>;
+    using Cfg = GradCfg<CONV>;
+    constexpr int STAGES = Cfg::STAGES, QSTAGES = CONV ? Cfg::QSTAGES : 1;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -333,11 +341,11 @@ __global__ void __launch_bounds__(kGradThreads, 1)
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < STAGES; ++s) {
-            // A's bytes and the group of converters of each CTA
-            mbar_init(bar_full + 8 * s, 1 + 2 * kGradConvWarps / kGradConvGroups);
+            // the loads' bytes, and the group of converters of each CTA
+            mbar_init(bar_full + 8 * s, CONV ? 1 + 2 * kGradConvWarps / kGradConvGroups : 1);
             mbar_init(bar_empty + 8 * s, 1);
         }
-        for (int s = 0; s < QSTAGES; ++s) {
+        for (int s = 0; CONV && s < QSTAGES; ++s) {
             mbar_init(bar_qfull + 8 * s, 1);
             mbar_init(bar_qempty + 8 * s, kGradConvWarps / kGradConvGroups);
         }
@@ -379,13 +387,20 @@ __global__ void __launch_bounds__(kGradThreads, 1)
                         break;
                     }
                     if (rank == 0)
-                        mbar_expect_tx(bar_full + 8 * s, 2 * Cfg::kABytes);
+                        mbar_expect_tx(bar_full + 8 * s,
+                                       2 * (Cfg::kABytes + (CONV ? 0 : Cfg::kBBytes)));
                     const uint32_t dst = sA + s * Cfg::kABytes;
                     if constexpr (WGRAD) {
                         tma_load_2d_pair(dst, &tmA, full0 + 8 * s, i0, kb * kGradBR);
                         tma_load_2d_pair(dst + 8192, &tmA, full0 + 8 * s, i0 + 64, kb * kGradBR);
                     } else {
                         tma_load_2d_pair(dst, &tmA, full0 + 8 * s, kb * kGradBR, i0);
+                    }
+                    if constexpr (!CONV) {
+                        const int j0 = jb * kGradTile + static_cast<int>(rank) * 128;
+                        const uint32_t b = sB + s * Cfg::kBBytes;
+                        tma_load_2d_pair(b, &tmQ, full0 + 8 * s, j0, kb * kGradBR);
+                        tma_load_2d_pair(b + 8192, &tmQ, full0 + 8 * s, j0 + 64, kb * kGradBR);
                     }
                 }
             }
@@ -396,7 +411,11 @@ __global__ void __launch_bounds__(kGradThreads, 1)
     } else if (warp == 1) {
         if (lane == 0 && rank == 0) {
             constexpr uint32_t idesc = idesc_bf16(kGradTile, kGradTile, WGRAD);
-            uint32_t it = 0, seg = 0;
+            // stage 0's descriptors; a stage further on adds its bytes / 16 to the address field
+            const uint64_t da = WGRAD ? sw128_mnmajor_desc(sA) : sw128_kmajor_desc(sA);
+            const uint64_t db = sw128_mnmajor_desc(sB);
+            constexpr uint32_t kStepA = (WGRAD ? 2048 : 32) / 16, kStepB = 2048 / 16;
+            uint32_t s = 0, ph = 0, seg = 0;
             bool ok = true;
             GradWalk walk(w, pair);
             GradSegment sg;
@@ -407,22 +426,24 @@ __global__ void __launch_bounds__(kGradThreads, 1)
                     break;
                 tc_fence_after();
                 const uint32_t d = tmem_base + buf * kGradTile;
-                for (int kb = sg.kb0; kb < sg.kb1; ++kb, ++it) {
-                    const uint32_t s = it % STAGES;
-                    if (!mbar_wait_cluster(bar_full + 8 * s, (it / STAGES) & 1u, limit_ns)) {
+                uint32_t accumulate = 0;
+                for (int n = sg.kb1 - sg.kb0; n > 0; --n) {
+                    if (!mbar_wait_cluster(bar_full + 8 * s, ph, limit_ns)) {
                         ok = false;
                         break;
                     }
                     tc_fence_after();
-                    const uint32_t a0 = sA + s * Cfg::kABytes, b0 = sB + s * Cfg::kBBytes;
+                    const uint64_t a0 = da + s * (Cfg::kABytes / 16), b0 = db + s * (Cfg::kBBytes / 16);
 #pragma unroll
-                    for (int k = 0; k < kGradBR / 16; ++k)
-                        umma_bf16_pair(d,
-                                       WGRAD ? sw128_mnmajor_desc(a0 + k * 2048)
-                                             : sw128_kmajor_desc(a0 + k * 32),
-                                       sw128_mnmajor_desc(b0 + k * 2048), idesc,
-                                       (kb > sg.kb0 || k > 0) ? 1u : 0u);
+                    for (int k = 0; k < kGradBR / 16; ++k) {
+                        umma_bf16_pair(d, a0 + k * kStepA, b0 + k * kStepB, idesc, accumulate);
+                        accumulate = 1;
+                    }
                     umma_commit_pair(bar_empty + 8 * s, 0x3);
+                    if (++s == STAGES) {
+                        s = 0;
+                        ph ^= 1u;
+                    }
                 }
                 if (ok)
                     umma_commit_pair(bar_tfull + 8 * buf, 0x3);
@@ -516,7 +537,7 @@ __global__ void __launch_bounds__(kGradThreads, 1)
             if (lane == 0)
                 mbar_arrive_cluster(tempty0 + 8 * buf); // the leader's accumulator is free
         }
-    } else if (warp == 2) {
+    } else if (CONV && warp == 2) {
         if (lane == 0) {
             pdl_wait();
             uint32_t it = 0;
@@ -540,7 +561,7 @@ __global__ void __launch_bounds__(kGradThreads, 1)
             if (ok)
                 drain_ring(bar_qempty, it, QSTAGES, limit_ns);
         }
-    } else if (warp >= kGradConvWarp0) {
+    } else if (CONV && warp >= kGradConvWarp0) {
         // converters: group g (four warps) takes every kGradConvGroups-th k-block, so the waits,
         // loads and fences of several k-blocks overlap. Two threads share a row r of the
         // k-block's [64 r][128 j] codes, every other 16-byte piece each, starting at the lane's
@@ -608,6 +629,32 @@ __global__ void __launch_bounds__(kGradThreads, 1)
     tc_fence_after();
     if (warp == 1)
         tmem_dealloc_pair(tmem_base, Cfg::kTmemCols);
+}
+
+// The whole of Q to scaled bf16 ahead of the product, [R, J]: 16 codes a thread and step.
+template <bool F8>
+__global__ void __launch_bounds__(256) grad_dequant_kernel(const uint8_t *__restrict__ q,
+                                                           const float *__restrict__ scale,
+                                                           int64_t nvec, uint32_t row_vecs,
+                                                           uint16_t *__restrict__ out)
+{
+    if (threadIdx.x == 0)
+        pdl_launch_dependents();
+    pdl_wait();
+    const int64_t stride = static_cast<int64_t>(gridDim.x) * blockDim.x;
+    for (int64_t v = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; v < nvec;
+         v += stride) {
+        const uint4 raw = ldg_nc_v4(reinterpret_cast<const uint4 *>(q) + v);
+        const uint32_t row = nvec <= 0xFFFFFFFFll
+                                 ? static_cast<uint32_t>(v) / row_vecs
+                                 : static_cast<uint32_t>(v / row_vecs);
+        const RowScale sc = row_scale(__ldg(scale + row));
+        const uint2 a = convert4<F8>(raw.x, sc), b = convert4<F8>(raw.y, sc);
+        const uint2 c = convert4<F8>(raw.z, sc), d = convert4<F8>(raw.w, sc);
+        uint4 *o = reinterpret_cast<uint4 *>(out) + 2 * v;
+        o[0] = make_uint4(a.x, a.y, b.x, b.y);
+        o[1] = make_uint4(c.x, c.y, d.x, d.y);
+    }
 }
 
 // Adds the partial tiles of the split tiles, in the order of the pairs, and finishes them: block

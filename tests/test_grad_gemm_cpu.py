@@ -48,11 +48,14 @@ def test_workspace_sizes(L):
     d, wg = L.w8a8_gemm_dgrad_workspace_size, L.w8a8_gemm_wgrad_workspace_size
     tile = 2 * 256 * 256 * 4  # two partial tiles per CTA pair
     assert d(1, 64, 256) == 0                       # one k-block: nothing to split
-    assert d(1, 8 * 64 * 2, 256) == 2 * tile        # 16 k-blocks, eight for each pair
+    assert d(1, 1024, 256) == 4 * tile              # 16 k-blocks, four for each pair
     assert d(4, 12, 64) == 0 and d(0, 64, 64) == 0  # refused shapes
     assert d(1, 4096, 4096) == 74 * tile            # 16 tiles of 64 k-blocks on 148 SMs
-    assert wg(64, 4096, 4096) == 0                  # short sums stay whole
-    assert wg(4096, 256, 256) == 8 * tile
+    assert d(2048, 72, 4096) == 72 * 4096 * 2       # many rows: the bf16 weight
+    assert wg(72, 4096, 4096) == 72 * 4096 * 2      # or the bf16 activations; short sums whole
+    assert wg(4096, 256, 256) == 16 * tile
+    # the bf16 operand (to 256 bytes), then the partial tiles of a split
+    assert d(1100, 8200, 272) == 8200 * 272 * 2 + 74 * tile
 
 
 def test_binding_refuses_cpu_tensors():
