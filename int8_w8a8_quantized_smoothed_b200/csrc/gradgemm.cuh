@@ -100,15 +100,15 @@ struct GradBlocks {
 // CONV: the kernel converts Q itself; otherwise B is a bf16 matrix loaded like A.
 template <bool CONV> struct GradCfg {
     static constexpr int STAGES = CONV ? 5 : 6;
-    static constexpr int QSTAGES = CONV ? 6 : 0;
+    static constexpr int QSTAGES = CONV ? 4 : 0;
     static constexpr int kThreads = CONV ? kGradThreads : 256; // without: no converter warps
     static constexpr int kABytes = 128 * kGradBR * 2;
     static constexpr int kBBytes = 128 * kGradBR * 2;
     static constexpr int kQBytes = 128 * kGradBR;
     static constexpr int kBOff = STAGES * kABytes;
     static constexpr int kQOff = kBOff + STAGES * kBBytes;
-    static constexpr int kOutOff = kQOff + QSTAGES * kQBytes; // 4 KB per epilogue warp
-    static constexpr int kBarOff = kOutOff + 4 * 4096;
+    static constexpr int kOutOff = kQOff + QSTAGES * kQBytes; // 2 x 4 KB per epilogue warp
+    static constexpr int kBarOff = kOutOff + 4 * 8192;
     // full[S], empty[S], qfull[QS], qempty[QS], tfull[2], tempty[2], tensor-memory slot
     static constexpr int kSmemBytes = kBarOff + (2 * STAGES + 2 * QSTAGES + 6) * 8 + 16 + 1024;
     static_assert(kSmemBytes <= 232448, "shared memory per CTA");
@@ -284,6 +284,8 @@ template <int ROW> __device__ __forceinline__ int stage_at(int r, int j)
     return r * ROW + (j ^ ((r * ROW >> 3) & (ROW - 1)));
 }
 
+// Asynchronous (cp.async): stage_load_wait<N> waits for all but the last N of the lane's loads
+// committed as groups; words outside the valid part keep what they held.
 template <int ROW>
 __device__ __forceinline__ void stage_load(uint4 *stage, int lane, const char *src, int64_t stride,
                                            int rows_valid, int bytes_valid)
@@ -291,11 +293,22 @@ __device__ __forceinline__ void stage_load(uint4 *stage, int lane, const char *s
 #pragma unroll
     for (int i = 0; i < ROW; ++i) {
         const int r = (i * 32 + lane) / ROW, j = lane % ROW;
-        uint4 x = make_uint4(0u, 0u, 0u, 0u);
         if (r < rows_valid && j * 16 < bytes_valid)
-            x = ldg_nc_v4(src + r * stride + j * 16);
-        stage[stage_at<ROW>(r, j)] = x;
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
+                             smem_u32(stage + stage_at<ROW>(r, j))),
+                         "l"(src + r * stride + j * 16)
+                         : "memory");
     }
+}
+
+__device__ __forceinline__ void stage_load_commit()
+{
+    asm volatile("cp.async.commit_group;" ::: "memory");
+}
+
+template <int N> __device__ __forceinline__ void stage_load_wait()
+{
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
 template <int ROW>
@@ -453,7 +466,7 @@ __global__ void __launch_bounds__(GradCfg<CONV>::kThreads, 1)
         // epilogue: this CTA's 128 rows of the tile, 32 per warp
         pdl_wait();
         const int quarter = warp & 3;
-        uint4 *stage_w = reinterpret_cast<uint4 *>(smem + Cfg::kOutOff) + quarter * 256;
+        uint4 *stage_w = reinterpret_cast<uint4 *>(smem + Cfg::kOutOff) + quarter * 512;
         const uint32_t tempty0 = map_peer_smem(bar_tempty, 0);
         uint32_t seg = 0;
         GradWalk walk(w, pair);
@@ -463,29 +476,38 @@ __global__ void __launch_bounds__(GradCfg<CONV>::kThreads, 1)
             tile_coords(sg.tile, w.ni, w.nj, w.group_i, ib, jb);
             const uint32_t buf = seg & 1u, aph = (seg >> 1) & 1u;
             ++seg;
-            if (!mbar_wait(bar_tfull + 8 * buf, aph, limit_ns))
-                break;
-            tc_fence_after();
-            const uint32_t tbase =
-                tmem_base + buf * kGradTile + (static_cast<uint32_t>(quarter * 32) << 16);
             const int row0 = ib * kGradTile + static_cast<int>(rank) * 128 + quarter * 32;
             const int rows = min(32, w.I - row0); // may be negative: nothing stored
             const int64_t ld = static_cast<int64_t>(w.J) * (SILU ? 4 : 2); // bytes
             float *slot = part + ((static_cast<int64_t>(pair) * 2 + sg.slot) * kGradTile +
                                   rank * 128 + quarter * 32) * kGradTile;
+            // SILU: the gate and up values of a chunk of 32 columns are on their way while the
+            // chunk before it is worked on, the first ones while the tile is still multiplied
+            auto fetch = [&](int c) {
+                const int j0 = jb * kGradTile + c * 32;
+                const char *gu = reinterpret_cast<const char *>(gate_up) + row0 * ld + j0 * 2;
+                const int bytes = min(64, (w.J - j0) * 2);
+                uint4 *to = stage_w + (c & 1) * 256;
+                stage_load<4>(to, lane, gu, ld, rows, bytes);
+                stage_load<4>(to + 128, lane, gu + static_cast<int64_t>(w.J) * 2, ld, rows, bytes);
+                stage_load_commit();
+            };
+            if constexpr (SILU)
+                if (!sg.partial)
+                    fetch(0);
+            if (!mbar_wait(bar_tfull + 8 * buf, aph, limit_ns))
+                break;
+            __syncwarp();
+            tc_fence_after();
+            const uint32_t tbase =
+                tmem_base + buf * kGradTile + (static_cast<uint32_t>(quarter * 32) << 16);
 #pragma unroll 1
             for (int c = 0; c < kGradTile / 32; ++c) {
                 const int j0 = jb * kGradTile + c * 32;
                 uint32_t r[32];
-                if constexpr (SILU) {
-                    if (!sg.partial) {
-                        const char *gu = reinterpret_cast<const char *>(gate_up) + row0 * ld + j0 * 2;
-                        const int bytes = min(64, (w.J - j0) * 2);
-                        stage_load<4>(stage_w, lane, gu, ld, rows, bytes);
-                        stage_load<4>(stage_w + 128, lane, gu + static_cast<int64_t>(w.J) * 2, ld,
-                                      rows, bytes);
-                    }
-                }
+                if constexpr (SILU)
+                    if (!sg.partial && c + 1 < kGradTile / 32)
+                        fetch(c + 1);
                 tmem_ld_32x32b_x32(tbase + c * 32, r);
                 tmem_ld_wait();
                 if (sg.partial) {
@@ -497,22 +519,27 @@ __global__ void __launch_bounds__(GradCfg<CONV>::kThreads, 1)
                     stage_store<8>(stage_w, lane, reinterpret_cast<char *>(slot + c * 32),
                                    kGradTile * 4, rows, 128);
                 } else if constexpr (SILU) {
+                    if (c + 1 < kGradTile / 32)
+                        stage_load_wait<1>();
+                    else
+                        stage_load_wait<0>();
                     __syncwarp();
+                    uint4 *st = stage_w + (c & 1) * 256;
 #pragma unroll
                     for (int e = 0; e < 4; ++e) { // the lane's own row, in place
                         float da[8];
 #pragma unroll
                         for (int i = 0; i < 8; ++i)
                             da[i] = __uint_as_float(r[e * 8 + i]);
-                        uint4 *g = stage_w + stage_at<4>(lane, e);
+                        uint4 *g = st + stage_at<4>(lane, e);
                         silu_grad8(da, g[0], g[128], g[0], g[128]);
                     }
                     __syncwarp();
                     char *dst = reinterpret_cast<char *>(out) + row0 * ld + j0 * 2;
                     const int bytes = min(64, (w.J - j0) * 2);
-                    stage_store<4>(stage_w, lane, dst, ld, rows, bytes);
-                    stage_store<4>(stage_w + 128, lane, dst + static_cast<int64_t>(w.J) * 2, ld,
-                                   rows, bytes);
+                    stage_store<4>(st, lane, dst, ld, rows, bytes);
+                    stage_store<4>(st + 128, lane, dst + static_cast<int64_t>(w.J) * 2, ld, rows,
+                                   bytes);
                 } else { // two chunks of columns go out together, 128 bytes a row
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
@@ -641,20 +668,53 @@ __global__ void __launch_bounds__(256) grad_dequant_kernel(const uint8_t *__rest
     if (threadIdx.x == 0)
         pdl_launch_dependents();
     pdl_wait();
+    // kFlight vectors of a thread in flight: the loads' latency, not HBM, set the pace with one
+    constexpr int kFlight = 4;
     const int64_t stride = static_cast<int64_t>(gridDim.x) * blockDim.x;
-    for (int64_t v = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; v < nvec;
-         v += stride) {
-        const uint4 raw = ldg_nc_v4(reinterpret_cast<const uint4 *>(q) + v);
-        const uint32_t row = nvec <= 0xFFFFFFFFll
-                                 ? static_cast<uint32_t>(v) / row_vecs
-                                 : static_cast<uint32_t>(v / row_vecs);
-        const RowScale sc = row_scale(__ldg(scale + row));
-        const uint2 a = convert4<F8>(raw.x, sc), b = convert4<F8>(raw.y, sc);
-        const uint2 c = convert4<F8>(raw.z, sc), d = convert4<F8>(raw.w, sc);
-        uint4 *o = reinterpret_cast<uint4 *>(out) + 2 * v;
-        o[0] = make_uint4(a.x, a.y, b.x, b.y);
-        o[1] = make_uint4(c.x, c.y, d.x, d.y);
+    for (int64_t v0 = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; v0 < nvec;
+         v0 += kFlight * stride) {
+        uint4 raw[kFlight];
+        float s[kFlight];
+#pragma unroll
+        for (int f = 0; f < kFlight; ++f) {
+            const int64_t v = v0 + f * stride;
+            if (v < nvec) {
+                raw[f] = ldg_nc_v4(reinterpret_cast<const uint4 *>(q) + v);
+                const uint32_t row = nvec <= 0xFFFFFFFFll
+                                         ? static_cast<uint32_t>(v) / row_vecs
+                                         : static_cast<uint32_t>(v / row_vecs);
+                s[f] = __ldg(scale + row);
+            }
+        }
+#pragma unroll
+        for (int f = 0; f < kFlight; ++f) {
+            const int64_t v = v0 + f * stride;
+            if (v < nvec) {
+                const RowScale sc = row_scale(s[f]);
+                const uint2 a = convert4<F8>(raw[f].x, sc), b = convert4<F8>(raw[f].y, sc);
+                const uint2 c = convert4<F8>(raw[f].z, sc), d = convert4<F8>(raw[f].w, sc);
+                uint4 *o = reinterpret_cast<uint4 *>(out) + 2 * v;
+                o[0] = make_uint4(a.x, a.y, b.x, b.y);
+                o[1] = make_uint4(c.x, c.y, d.x, d.y);
+            }
+        }
     }
+}
+
+// The pair whose range of the split holds unit v, in 32 bits where they do.
+__device__ __forceinline__ int split_owner(int64_t v, int64_t U, int pairs)
+{
+    if (U * pairs < 0x7FFFFFFF) {
+        const uint32_t u = static_cast<uint32_t>(U), n = static_cast<uint32_t>(pairs);
+        const uint32_t x = static_cast<uint32_t>(v);
+        uint32_t c = x * n / u;
+        while (c + 1 < n && (c + 1) * u / n <= x)
+            ++c;
+        while (c > 0 && c * u / n > x)
+            --c;
+        return static_cast<int>(c);
+    }
+    return static_cast<int>(sk_owner_of(v, U, pairs));
 }
 
 // Adds the partial tiles of the split tiles, in the order of the pairs, and finishes them: block
@@ -678,22 +738,37 @@ __global__ void __launch_bounds__(256) grad_fixup_kernel(const GradWork w,
         return;
     const int64_t U = static_cast<int64_t>(w.rem) * w.kblocks;
     const int64_t u0 = static_cast<int64_t>(t) * w.kblocks;
-    const int p0 = static_cast<int>(sk_owner_of(u0, U, w.rem_pairs));
-    const int p1 = static_cast<int>(sk_owner_of(u0 + w.kblocks - 1, U, w.rem_pairs));
+    const int p0 = split_owner(u0, U, w.rem_pairs);
+    const int p1 = split_owner(u0 + w.kblocks - 1, U, w.rem_pairs);
     if (p0 == p1)
         return; // one pair had the whole tile and finished it
     float f[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i)
         f[i] = 0.0f;
-    for (int p = p0; p <= p1; ++p) {
-        const int64_t begin = p * U / w.rem_pairs;
-        const int slot = static_cast<int>(begin / w.kblocks) != t;
-        const float4 *src = reinterpret_cast<const float4 *>(
-            part + ((static_cast<int64_t>(p) * 2 + slot) * kGradTile + rl) * kGradTile + cl);
-        const float4 a = src[0], b = src[1];
-        f[0] += a.x; f[1] += a.y; f[2] += a.z; f[3] += a.w;
-        f[4] += b.x; f[5] += b.y; f[6] += b.z; f[7] += b.w;
+    // Only the first pair can have begun in an earlier tile (its slot 1); the others' ranges begin
+    // here. Four parts are in flight, added in order.
+    const float4 *src = reinterpret_cast<const float4 *>(
+        part + (static_cast<int64_t>(p0) * 2 * kGradTile + rl) * kGradTile + cl);
+    constexpr int kSlot = kGradTile * kGradTile / 4;
+    const bool second = static_cast<int64_t>(p0) * U / w.rem_pairs < u0;
+    for (int p = p0; p <= p1; p += 4) {
+        float4 v[4][2];
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            if (p + e <= p1) {
+                const float4 *at = src + static_cast<int64_t>(p + e - p0) * 2 * kSlot +
+                                   (second && p + e == p0 ? kSlot : 0);
+                v[e][0] = __ldcs(at);
+                v[e][1] = __ldcs(at + 1);
+            }
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            if (p + e <= p1) {
+                const float4 a = v[e][0], b = v[e][1];
+                f[0] += a.x; f[1] += a.y; f[2] += a.z; f[3] += a.w;
+                f[4] += b.x; f[5] += b.y; f[6] += b.z; f[7] += b.w;
+            }
     }
     if constexpr (SILU) {
         const int64_t o = static_cast<int64_t>(row) * 2 * w.J + col;
