@@ -186,27 +186,38 @@ int check_grad_shape(int64_t M, int64_t N, int64_t K)
     return W8A8_OK;
 }
 
+enum GradForm { kGradNarrow, kGradConv, kGradDequant };
+
 struct GradPlan {
     GradWork w;
-    bool conv;          // the GEMM converts Q itself; otherwise Q goes through a bf16 workspace
-    size_t part_off;    // partial tiles of a split, after the bf16 operand
+    GradForm form;
+    int nt;          // rows of a narrow tile
+    size_t part_off; // partial tiles of a split, after the bf16 operand
     size_t ws_bytes;
 };
 
+// Up to this many rows i an input gradient runs the narrow kernel.
+constexpr int64_t kGradNarrowRows = 128;
 // From this many rows i on, Q is converted once ahead of the product. The kernel that converts
 // its tiles itself does each of them again for every 256 rows and runs at about 1.1 PFLOP/s, the
-// other at about 1.5, after a pass over Q of 3 bytes a code.
+// other at about 1.4, after a pass over Q of 3 bytes a code.
 constexpr int64_t kGradDequantRows = 1024;
 
 // False when there are more tiles than an int counts.
-bool grad_plan(int64_t I, int64_t J, int64_t R, int sms, GradPlan *p)
+bool grad_plan(int64_t I, int64_t J, int64_t R, bool wgrad, int sms, GradPlan *p)
 {
-    const int64_t ni = (I + kGradTile - 1) / kGradTile, nj = (J + kGradTile - 1) / kGradTile;
-    const int64_t tiles = ni * nj, kb = (R + kGradBR - 1) / kGradBR, pairs = sms / 2;
+    GradWork *w = &p->w;
+    p->form = I >= kGradDequantRows ? kGradDequant
+              : !wgrad && I <= kGradNarrowRows ? kGradNarrow : kGradConv;
+    const bool narrow = p->form == kGradNarrow;
+    p->nt = I <= 16 ? 16 : I <= 32 ? 32 : I <= 64 ? 64 : 128;
+    w->tile_i = narrow ? p->nt : kGradTile;
+    w->tile_j = narrow ? 128 : kGradTile;
+    const int64_t ni = (I + w->tile_i - 1) / w->tile_i, nj = (J + w->tile_j - 1) / w->tile_j;
+    const int64_t tiles = ni * nj, kb = (R + kGradBR - 1) / kGradBR;
+    const int64_t pairs = narrow ? sms : sms / 2;
     if (tiles > (1 << 30))
         return false;
-    GradWork *w = &p->w;
-    p->conv = I < kGradDequantRows;
     w->I = static_cast<int>(I);
     w->J = static_cast<int>(J);
     w->R = static_cast<int>(R);
@@ -219,19 +230,22 @@ bool grad_plan(int64_t I, int64_t J, int64_t R, int sms, GradPlan *p)
     w->rem = static_cast<int>(tiles % pairs);
     w->rem_pairs = w->rem;
     if (w->rem > 0) {
-        // The last tiles' k-blocks are split over all pairs where that saves more time than the
-        // partial tiles cost: a k-block takes 0.55 us (converted here) or 0.35 us; the second
-        // launch about 4 us, storing and adding partial tiles up to 8 us (by their rows).
+        // The last tiles' k-blocks are split over all pairs (CTAs) where that saves more time
+        // than the partial tiles cost: a k-block takes about 0.2 us (narrow), 0.55 us (converted
+        // by the kernel) or 0.35 us; the second launch about 4 us, storing and adding partial
+        // tiles up to 8 us (by their rows).
         const int64_t split = std::min(pairs, std::max<int64_t>(w->rem, w->rem * kb / 4));
-        const double each = p->conv ? 0.55 : 0.35;
+        const double each = narrow ? 0.2 : p->form == kGradConv ? 0.55 : 0.35;
         const double saved = each * (kb - static_cast<double>(w->rem * kb) / split);
-        if (saved > 4.0 + 8.0 * std::min<int64_t>(I, kGradTile) / kGradTile)
+        if (saved > 4.0 + (narrow ? 0.0 : 8.0 * std::min<int64_t>(I, kGradTile) / kGradTile))
             w->rem_pairs = static_cast<int>(split);
     }
-    p->part_off = p->conv ? 0 : (static_cast<size_t>(R) * static_cast<size_t>(J) * 2 + 255) / 256 * 256;
+    p->part_off = p->form == kGradDequant
+                      ? (static_cast<size_t>(R) * static_cast<size_t>(J) * 2 + 255) / 256 * 256
+                      : 0;
     p->ws_bytes = p->part_off;
     if (w->rem_pairs > w->rem)
-        p->ws_bytes += static_cast<size_t>(w->rem_pairs) * 2 * kGradTile * kGradTile * sizeof(float);
+        p->ws_bytes += static_cast<size_t>(w->rem_pairs) * 2 * w->tile_i * w->tile_j * sizeof(float);
     return true;
 }
 
@@ -252,6 +266,22 @@ int encode_grad(CUtensorMap *map, const void *base, int64_t rows, int64_t inner,
     return r == CUDA_SUCCESS ? W8A8_OK : W8A8_ERR_CUDA;
 }
 
+// The second launch, where tiles were split.
+template <bool SILU>
+int launch_fixup(const GradWork &w, const float *part, const uint16_t *gate_up, uint16_t *out,
+                 int dev, cudaStream_t st)
+{
+    if (w.rem_pairs <= w.rem)
+        return W8A8_OK;
+    const void *fn = reinterpret_cast<const void *>(&grad_fixup_kernel<SILU>);
+    if (int rc = ensure_smem(fn, dev, 0))
+        return rc;
+    const unsigned values = static_cast<unsigned>(std::min(w.I, w.tile_i) * w.tile_j);
+    return launch_kernel(grad_fixup_kernel<SILU>,
+                         dim3((values + 2047) / 2048, static_cast<unsigned>(w.rem)), dim3(256), 0,
+                         st, w, part, gate_up, out);
+}
+
 template <bool CONV, bool WGRAD, bool F8, bool SILU>
 int launch_grad(const CUtensorMap &ta, const CUtensorMap &tq, const float *scale,
                 const GradWork &w, const uint16_t *gate_up, uint16_t *out, float *part, int dev,
@@ -266,14 +296,36 @@ int launch_grad(const CUtensorMap &ta, const CUtensorMap &tq, const float *scale
                                        Cfg::kSmemBytes, st, 2u, ta, tq, scale, w, gate_up, out,
                                        part, kWaitLimitNs))
         return rc;
-    if (w.rem_pairs <= w.rem)
-        return W8A8_OK; // no tile was split
-    const void *fix = reinterpret_cast<const void *>(&grad_fixup_kernel<SILU>);
-    if (int rc = ensure_smem(fix, dev, 0))
+    return launch_fixup<SILU>(w, part, gate_up, out, dev, st);
+}
+
+template <int NT, bool F8, bool SILU>
+int launch_narrow(const CUtensorMap &ta, const CUtensorMap &tq, const float *scale,
+                  const GradWork &w, const uint16_t *gate_up, uint16_t *out, float *part, int dev,
+                  cudaStream_t st)
+{
+    using Cfg = NarrowCfg<NT>;
+    auto kernel = grad_narrow_kernel<NT, F8, SILU>;
+    if (int rc = ensure_smem(reinterpret_cast<const void *>(kernel), dev, Cfg::kSmemBytes))
         return rc;
-    const unsigned rows = static_cast<unsigned>(std::min(w.I, kGradTile));
-    return launch_kernel(grad_fixup_kernel<SILU>, dim3((rows + 7) / 8, static_cast<unsigned>(w.rem)),
-                         dim3(256), 0, st, w, static_cast<const float *>(part), gate_up, out);
+    const unsigned ctas = static_cast<unsigned>(w.whole > 0 ? w.npairs : w.rem_pairs);
+    if (int rc = launch_kernel(kernel, dim3(ctas), dim3(kNarrowThreads), Cfg::kSmemBytes, st, ta,
+                               tq, scale, w, gate_up, out, part, kWaitLimitNs))
+        return rc;
+    return launch_fixup<SILU>(w, part, gate_up, out, dev, st);
+}
+
+template <bool F8, bool SILU>
+int launch_narrow_nt(int nt, const CUtensorMap &ta, const CUtensorMap &tq, const float *scale,
+                     const GradWork &w, const uint16_t *gate_up, uint16_t *out, float *part,
+                     int dev, cudaStream_t st)
+{
+    switch (nt) {
+    case 16: return launch_narrow<16, F8, SILU>(ta, tq, scale, w, gate_up, out, part, dev, st);
+    case 32: return launch_narrow<32, F8, SILU>(ta, tq, scale, w, gate_up, out, part, dev, st);
+    case 64: return launch_narrow<64, F8, SILU>(ta, tq, scale, w, gate_up, out, part, dev, st);
+    default: return launch_narrow<128, F8, SILU>(ta, tq, scale, w, gate_up, out, part, dev, st);
+    }
 }
 
 template <bool F8>
@@ -311,18 +363,25 @@ int grad_impl(bool f8, const uint16_t *dy, const void *q, const float *scale, in
         return rc;
     const int64_t R = WGRAD ? M : N;
     GradPlan p;
-    if (!grad_plan(WGRAD ? N : M, K, R, sms, &p))
+    if (!grad_plan(WGRAD ? N : M, K, R, WGRAD, sms, &p))
         return W8A8_ERR_UNSUPPORTED_SHAPE;
     if (p.ws_bytes > 0 && (workspace == nullptr || workspace_bytes < p.ws_bytes))
         return W8A8_ERR_WORKSPACE;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     float *part = reinterpret_cast<float *>(static_cast<char *>(workspace) + p.part_off);
     CUtensorMap ta, tq;
-    if (encode_grad(&ta, dy, M, N, 2, WGRAD ? kGradBR : 128, true))
+    const int box_i = p.form == kGradNarrow ? p.nt : 128;
+    if (encode_grad(&ta, dy, M, N, 2, WGRAD ? kGradBR : box_i, true))
         return W8A8_ERR_CUDA;
-    if (p.conv) {
-        if (encode_grad(&tq, q, R, K, 1, kGradBR, false))
+    if (p.form != kGradDequant) {
+        if (encode_grad(&tq, q, R, K, 1, kGradBR, p.form == kGradNarrow))
             return W8A8_ERR_CUDA;
+        if constexpr (!WGRAD)
+            if (p.form == kGradNarrow)
+                return f8 ? launch_narrow_nt<true, SILU>(p.nt, ta, tq, scale, p.w, gate_up, out,
+                                                         part, dev, st)
+                          : launch_narrow_nt<false, SILU>(p.nt, ta, tq, scale, p.w, gate_up, out,
+                                                          part, dev, st);
         return f8 ? launch_grad<true, WGRAD, true, SILU>(ta, tq, scale, p.w, gate_up, out, part,
                                                          dev, st)
                   : launch_grad<true, WGRAD, false, SILU>(ta, tq, scale, p.w, gate_up, out, part,
@@ -345,7 +404,7 @@ size_t grad_workspace(int64_t M, int64_t N, int64_t K, bool wgrad)
     if (current_device(&dev, &sms))
         sms = 148;
     GradPlan p;
-    return grad_plan(wgrad ? N : M, K, wgrad ? M : N, sms, &p) ? p.ws_bytes : 0;
+    return grad_plan(wgrad ? N : M, K, wgrad ? M : N, wgrad, sms, &p) ? p.ws_bytes : 0;
 }
 
 } // namespace

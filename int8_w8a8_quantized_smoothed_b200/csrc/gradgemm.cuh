@@ -32,8 +32,9 @@ constexpr int kGradBR = 64;    // r per k-block: one 128-byte row of bf16
 // evenly over rem_pairs pairs, whose partial tiles grad_fixup_kernel adds.
 struct GradWork {
     int I, J, R;
+    int tile_i, tile_j; // 256 x 256 for a CTA pair; narrow kernel: 16 .. 128 x 128 for a CTA
     int ni, nj, kblocks, group_i;
-    int npairs, whole, rem, rem_pairs;
+    int npairs, whole, rem, rem_pairs; // (narrow kernel: CTAs)
 };
 
 struct GradSegment {
@@ -127,15 +128,15 @@ __device__ __forceinline__ void umma_bf16_pair(uint32_t d_tmem, uint64_t a_desc,
         : "memory");
 }
 
-// Instruction descriptor of kind::f16 with bf16 A and B and a binary32 D; B is MN-major, A
-// K-major or MN-major.
-__host__ __device__ constexpr uint32_t idesc_bf16(int m, int n, bool a_mn)
+// Instruction descriptor of kind::f16 with bf16 A and B and a binary32 D, each operand K-major or
+// MN-major.
+__host__ __device__ constexpr uint32_t idesc_bf16(int m, int n, bool a_mn, bool b_mn)
 {
     return (1u << 4)                                // D format: F32
            | (1u << 7)                              // A format: BF16
            | (1u << 10)                             // B format: BF16
            | ((a_mn ? 1u : 0u) << 15)               // A MN-major
-           | (1u << 16)                             // B MN-major
+           | ((b_mn ? 1u : 0u) << 16)               // B MN-major
            | (static_cast<uint32_t>(n >> 3) << 17)  // N / 8
            | (static_cast<uint32_t>(m >> 4) << 24); // M / 16
 }
@@ -203,33 +204,32 @@ __device__ __forceinline__ uint32_t fma_bf16x2(uint32_t a, uint32_t b, uint32_t 
     return r;
 }
 
-// A row's scale as the sum of two bf16 values (the nearest one and the nearest to what it leaves,
-// 2^-17 relative together), each in both halves of a word.
+// A scale as the sum of two bf16 values, the nearest one and the nearest to what it leaves (2^-17
+// relative together), in the upper halves of hi and lo.
+__device__ __forceinline__ void split_scale(float s, uint32_t &hi, uint32_t &lo)
+{
+    hi = __float_as_uint(s) + 0x8000u;
+    lo = __float_as_uint(s - __uint_as_float(hi & 0xFFFF0000u)) + 0x8000u;
+}
+
+// The same with each part in both halves of a word.
 struct RowScale {
     uint32_t hi, lo;
 };
 
 __device__ __forceinline__ RowScale row_scale(float s)
 {
-    RowScale r;
-    const uint32_t h = __float_as_uint(s) + 0x8000u;
-    r.hi = __byte_perm(h, h, 0x3232);
-    const uint32_t l = __float_as_uint(s - __uint_as_float(h & 0xFFFF0000u)) + 0x8000u;
-    r.lo = __byte_perm(l, l, 0x3232);
-    return r;
+    uint32_t h, l;
+    split_scale(s, h, l);
+    return RowScale{__byte_perm(h, h, 0x3232), __byte_perm(l, l, 0x3232)};
 }
 
-// Four codes (one 32-bit word) to bf16(s q), in packed bf16 arithmetic: a conversion instruction
-// (cvt.rn.bf16x2.f32) for each pair held the kernel at 1000 cycles a k-block, its pipe 90% busy.
-// q is exact in bf16, and q hi + bf16(q lo) is rounded once, so the result is bf16 of s q within
-// 2^-16 relative.
+// Four codes (a 32-bit word) as exact bf16 values, v[0] the first two.
 // INT8: the low 7 bits as the fraction of 128 make 128 + (q & 127), the sign bit as the lowest
 // exponent bit of 128 makes 128 or 256; their difference is q.
 // E4M3: exponent and fraction moved to a bf16's places make q 2^-120 (subnormals too).
-template <bool F8>
-__device__ __forceinline__ uint2 convert4(uint32_t w, const RowScale sc)
+template <bool F8> __device__ __forceinline__ void code_values(uint32_t w, uint32_t (&v)[2])
 {
-    uint32_t v[2];
     if constexpr (F8) {
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
@@ -243,6 +243,15 @@ __device__ __forceinline__ uint2 convert4(uint32_t w, const RowScale sc)
             v[k] = sub_bf16x2(__byte_perm(m, 0x43434343u, k ? 0x4342 : 0x4140),
                               __byte_perm(n, 0x43434343u, k ? 0x4342 : 0x4140));
     }
+}
+
+// Four codes of one row to bf16(s q), in packed bf16 arithmetic: q hi + bf16(q lo) is rounded once,
+// so the result is bf16 of s q within 2^-16 relative.
+template <bool F8>
+__device__ __forceinline__ uint2 convert4(uint32_t w, const RowScale sc)
+{
+    uint32_t v[2];
+    code_values<F8>(w, v);
     return make_uint2(fma_bf16x2(v[0], sc.hi, mul_bf16x2(v[0], sc.lo)),
                       fma_bf16x2(v[1], sc.hi, mul_bf16x2(v[1], sc.lo)));
 }
@@ -423,7 +432,7 @@ __global__ void __launch_bounds__(GradCfg<CONV>::kThreads, 1)
         }
     } else if (warp == 1) {
         if (lane == 0 && rank == 0) {
-            constexpr uint32_t idesc = idesc_bf16(kGradTile, kGradTile, WGRAD);
+            constexpr uint32_t idesc = idesc_bf16(kGradTile, kGradTile, WGRAD, true);
             // stage 0's descriptors; a stage further on adds its bytes / 16 to the address field
             const uint64_t da = WGRAD ? sw128_mnmajor_desc(sA) : sw128_kmajor_desc(sA);
             const uint64_t db = sw128_mnmajor_desc(sB);
@@ -658,6 +667,413 @@ __global__ void __launch_bounds__(GradCfg<CONV>::kThreads, 1)
         tmem_dealloc_pair(tmem_base, Cfg::kTmemCols);
 }
 
+// ---------------------------------------------------------------- few rows (input gradients)
+//
+// For at most 128 rows i the MMAs of a 256 x 256 tile would be mostly empty, and each SM should do
+// nothing but stream its share of the codes. Here a CTA takes 128 columns j and all rows i, and the
+// converted operand is the MMA's first one, in tensor memory: D^T = B^T A^T with j on the 128
+// lanes, i along 16 .. 128 columns. Q's tile is transposed on its way (rows r of bytes j, to lanes
+// j of values r) by the byte form of ldmatrix, whose register layout is the one that the 16x256b
+// store to tensor memory takes, so it is neither stored to shared memory again nor waited for by a
+// proxy fence. (With 256 rows this form is the slower one: an MMA whose first operand is in tensor
+// memory took 690 cycles a k-block where the pair's took 610.) The scales, which here vary along
+// a register's bytes, come from shared memory, prepared by a warp of their own.
+
+// warps: 0 A producer, 1 MMA, 2 Q producer, 3 scales; 4 .. 7 epilogue; 8 .. 23 converters
+constexpr int kNarrowThreads = 768;
+constexpr int kNarrowConvWarp0 = 8;
+constexpr int kNarrowGroups = 4; // groups of four converter warps, each on its own k-block
+
+template <int NT> struct NarrowCfg {
+    static constexpr int STAGES = 8, QSTAGES = NT == 128 ? 8 : 10;
+    static constexpr int kABytes = NT * kGradBR * 2;
+    static constexpr int kQBytes = 128 * kGradBR;
+    static constexpr int kQOff = STAGES * kABytes;
+    static constexpr int kScOff = kQOff + QSTAGES * kQBytes; // 16 bytes for four r's scales
+    static constexpr int kScBytes = kGradBR / 4 * 16;
+    static constexpr int kOutOff = kScOff + QSTAGES * kScBytes; // 4 KB per epilogue warp
+    static constexpr int kBarOff = kOutOff + 4 * 4096;
+    // full[S], empty[S], qfull[QS], qempty[QS], tfull[2], tempty[2], tensor-memory slot
+    static constexpr int kSmemBytes = kBarOff + (2 * STAGES + 2 * QSTAGES + 4) * 8 + 16 + 1024;
+    static_assert(kSmemBytes <= 232448, "shared memory per CTA");
+    // two accumulators of 128 lanes j x NT columns i, then the converted operand's stages
+    static constexpr int kTmemCols = 512;
+    static constexpr int kTmemB = 256;
+    static_assert(2 * NT <= kTmemB && kTmemB + STAGES * kGradBR / 2 <= kTmemCols, "tensor memory");
+};
+
+// D (+)= A B^T with A in tensor memory and B in shared memory, bf16.
+__device__ __forceinline__ void umma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
+                                             uint32_t idesc, uint32_t accumulate)
+{
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+// Two 16 x 16 byte matrices (16 rows of 16 bytes each; lanes 0 .. 15 give the first one's row
+// addresses, 16 .. 31 the second's), transposed: lane t gets bytes 4 (t % 4) .. + 3 of row t / 4
+// in r[0] and of row t / 4 + 8 in r[1], and of the second matrix in r[2], r[3].
+__device__ __forceinline__ void ldmatrix_b8_trans_x2(uint32_t addr, uint32_t (&r)[4])
+{
+    asm volatile("ldmatrix.sync.aligned.m16n16.x2.trans.shared.b8 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+
+// 16 lanes x 32 columns of tensor memory: of column group g (8 columns), lane t stores r[4g],
+// r[4g + 1] to columns 2 (t % 4), + 1 of lane t / 4 and r[4g + 2], r[4g + 3] to those of lane
+// t / 4 + 8.
+__device__ __forceinline__ void tmem_st_16x256b_x4(uint32_t taddr, const uint32_t (&r)[16])
+{
+    asm volatile("tcgen05.st.sync.aligned.16x256b.x4.b32 [%0],"
+                 " {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(
+                     taddr),
+                 "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]),
+                 "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]),
+                 "r"(r[14]), "r"(r[15])
+                 : "memory");
+}
+
+__device__ __forceinline__ void tmem_st_wait()
+{
+    asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+
+// Four codes (rows r .. r + 3 of one column, a byte each) to bf16(s q): convert4 with two scales'
+// parts in a word. sc: the hi parts of r, r + 1 and of r + 2, r + 3, then the lo parts.
+template <bool F8>
+__device__ __forceinline__ void convert4_rows(uint32_t w, const uint4 sc, uint32_t &o0, uint32_t &o1)
+{
+    uint32_t v[2];
+    code_values<F8>(w, v);
+    o0 = fma_bf16x2(v[0], sc.x, mul_bf16x2(v[0], sc.z));
+    o1 = fma_bf16x2(v[1], sc.y, mul_bf16x2(v[1], sc.w));
+}
+
+// Two 16-byte words, `second` and `first` by turns, from a staging buffer whose readers' rows are
+// 128 bytes apart: lanes of odd rows read the second word first, so eight lanes fill all banks.
+__device__ __forceinline__ void read_pair(const uint4 *p, int odd, uint4 &first, uint4 &second)
+{
+    const uint4 a = p[odd], b = p[odd ^ 1];
+    first = odd ? b : a;
+    second = odd ? a : b;
+}
+
+template <int NT, bool F8, bool SILU>
+__global__ void __launch_bounds__(kNarrowThreads, 1)
+    grad_narrow_kernel(const __grid_constant__ CUtensorMap tmA,
+                     const __grid_constant__ CUtensorMap tmQ, const float *__restrict__ scale,
+                     const GradWork w, const uint16_t *__restrict__ gate_up,
+                     uint16_t *__restrict__ out, float *__restrict__ part,
+                     unsigned long long limit_ns)
+{
+    using Cfg = NarrowCfg<NT>;
+    constexpr int STAGES = Cfg::STAGES, QSTAGES = Cfg::QSTAGES;
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>(
+        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+    const uint32_t sbase = smem_u32(smem);
+    const uint32_t sA = sbase, sQ = sbase + Cfg::kQOff;
+    const uint32_t bar_full = sbase + Cfg::kBarOff;
+    const uint32_t bar_empty = bar_full + 8 * STAGES;
+    const uint32_t bar_qfull = bar_empty + 8 * STAGES;
+    const uint32_t bar_qempty = bar_qfull + 8 * QSTAGES;
+    const uint32_t bar_tfull = bar_qempty + 8 * QSTAGES;
+    const uint32_t bar_tempty = bar_tfull + 16;
+    const uint32_t tslot = bar_tempty + 16;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int cta = blockIdx.x;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < STAGES; ++s) {
+            mbar_init(bar_full + 8 * s, 1 + 4); // A's bytes, four converter warps
+            mbar_init(bar_empty + 8 * s, 1);
+        }
+        for (int s = 0; s < QSTAGES; ++s) {
+            mbar_init(bar_qfull + 8 * s, 2); // Q's bytes, the scales
+            mbar_init(bar_qempty + 8 * s, 4);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(bar_tfull + 8 * b, 1);
+            mbar_init(bar_tempty + 8 * b, 4);
+        }
+        fence_mbar_init();
+        tma_prefetch_desc(&tmA);
+        tma_prefetch_desc(&tmQ);
+    }
+    __syncwarp();
+    if (warp == 1)
+        tmem_alloc(tslot, Cfg::kTmemCols);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem_base =
+        *reinterpret_cast<volatile uint32_t *>(smem + (tslot - sbase));
+
+    if (warp == 0) {
+        if (lane == 0) {
+            pdl_wait();
+            uint32_t it = 0;
+            bool ok = true;
+            GradWalk walk(w, cta);
+            GradSegment sg;
+            while (ok && walk.next(w, sg)) {
+                for (int kb = sg.kb0; kb < sg.kb1; ++kb, ++it) {
+                    const uint32_t s = it % STAGES;
+                    if (!mbar_wait(bar_empty + 8 * s, ((it / STAGES) & 1u) ^ 1u, limit_ns)) {
+                        ok = false;
+                        break;
+                    }
+                    mbar_expect_tx(bar_full + 8 * s, Cfg::kABytes);
+                    tma_load_2d(sA + s * Cfg::kABytes, &tmA, bar_full + 8 * s, kb * kGradBR, 0);
+                }
+            }
+            if (ok) // every stage released by the MMAs before this CTA may leave
+                drain_ring(bar_empty, it, STAGES, limit_ns);
+            pdl_launch_dependents();
+        }
+    } else if (warp == 1) {
+        if (lane == 0) {
+            constexpr uint32_t idesc = idesc_bf16(128, NT, false, false);
+            uint32_t it = 0, seg = 0;
+            bool ok = true;
+            GradWalk walk(w, cta);
+            GradSegment sg;
+            while (ok && walk.next(w, sg)) {
+                const uint32_t buf = seg & 1u, aph = (seg >> 1) & 1u;
+                ++seg;
+                if (!mbar_wait(bar_tempty + 8 * buf, aph ^ 1u, limit_ns))
+                    break;
+                tc_fence_after();
+                for (int kb = sg.kb0; kb < sg.kb1; ++kb, ++it) {
+                    const uint32_t s = it % STAGES;
+                    if (!mbar_wait(bar_full + 8 * s, (it / STAGES) & 1u, limit_ns)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint64_t a0 = sw128_kmajor_desc(sA + s * Cfg::kABytes);
+                    const uint32_t b0 = tmem_base + Cfg::kTmemB + s * (kGradBR / 2);
+#pragma unroll
+                    for (int k = 0; k < kGradBR / 16; ++k)
+                        umma_bf16_ts(tmem_base + buf * NT, b0 + k * 8, a0 + k * 2, idesc,
+                                     (kb > sg.kb0 || k > 0) ? 1u : 0u);
+                    umma_commit(bar_empty + 8 * s);
+                }
+                if (ok)
+                    umma_commit(bar_tfull + 8 * buf);
+            }
+        }
+    } else if (warp == 2) {
+        if (lane == 0) {
+            pdl_wait();
+            uint32_t it = 0;
+            bool ok = true;
+            GradWalk walk(w, cta);
+            GradSegment sg;
+            while (ok && walk.next(w, sg)) {
+                const int j0 = sg.tile * 128;
+                for (int kb = sg.kb0; kb < sg.kb1; ++kb, ++it) {
+                    const uint32_t s = it % QSTAGES;
+                    if (!mbar_wait(bar_qempty + 8 * s, ((it / QSTAGES) & 1u) ^ 1u, limit_ns)) {
+                        ok = false;
+                        break;
+                    }
+                    mbar_expect_tx(bar_qfull + 8 * s, Cfg::kQBytes);
+                    tma_load_2d(sQ + s * Cfg::kQBytes, &tmQ, bar_qfull + 8 * s, j0, kb * kGradBR);
+                }
+            }
+            if (ok)
+                drain_ring(bar_qempty, it, QSTAGES, limit_ns);
+        }
+    } else if (warp == 3) {
+        // the k-block's scales as convert4 takes them: lane l < 16 those of r = 4 l .. 4 l + 3
+        pdl_wait();
+        float next[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        auto fetch = [&](int kb) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int r = kb * kGradBR + 4 * lane + e;
+                next[e] = lane < kGradBR / 4 && r < w.R ? __ldg(scale + r) : 0.0f;
+            }
+        };
+        GradBlocks blk(w, cta, 0);
+        if (blk.ok)
+            fetch(blk.kb);
+        for (uint32_t it = 0; blk.ok; ++it) {
+            uint32_t hi[4], lo[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                split_scale(next[e], hi[e], lo[e]);
+            blk.advance(w, 1);
+            if (blk.ok)
+                fetch(blk.kb); // a k-block early
+            const uint32_t s = it % QSTAGES;
+            if (!mbar_wait(bar_qempty + 8 * s, ((it / QSTAGES) & 1u) ^ 1u, limit_ns))
+                break;
+            if (lane < kGradBR / 4)
+                reinterpret_cast<uint4 *>(smem + Cfg::kScOff + s * Cfg::kScBytes)[lane] =
+                    make_uint4(__byte_perm(hi[0], hi[1], 0x7632), __byte_perm(hi[2], hi[3], 0x7632),
+                               __byte_perm(lo[0], lo[1], 0x7632), __byte_perm(lo[2], lo[3], 0x7632));
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(bar_qfull + 8 * s);
+        }
+    } else if (warp < kNarrowConvWarp0) {
+        // epilogue: the warp's lanes are 32 columns j; the rows i in chunks of 32
+        pdl_wait();
+        const int quarter = warp & 3;
+        uint4 *stage = reinterpret_cast<uint4 *>(smem + Cfg::kOutOff) + quarter * 256;
+        uint32_t *words = reinterpret_cast<uint32_t *>(stage);
+        uint32_t seg = 0;
+        GradWalk walk(w, cta);
+        GradSegment sg;
+        while (walk.next(w, sg)) {
+            const uint32_t buf = seg & 1u, aph = (seg >> 1) & 1u;
+            ++seg;
+            if (!mbar_wait(bar_tfull + 8 * buf, aph, limit_ns))
+                break;
+            __syncwarp();
+            tc_fence_after();
+            const uint32_t tbase = tmem_base + buf * NT + (static_cast<uint32_t>(quarter * 32) << 16);
+            const int jl = quarter * 32;
+            const int j0 = sg.tile * 128 + jl;
+            float *slot = part + (static_cast<int64_t>(cta) * 2 + sg.slot) * NT * 128 + jl + lane;
+#pragma unroll 1
+            for (int c = 0; c < (NT + 31) / 32; ++c) {
+                const int i0 = c * 32;
+                uint32_t r[32]; // of 16 rows' accumulator: columns past it, never stored
+                tmem_ld_32x32b_x32(tbase + c * 32, r);
+                tmem_ld_wait();
+                if (c == (NT + 31) / 32 - 1) { // the accumulator is in registers
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0)
+                        mbar_arrive(bar_tempty + 8 * buf);
+                }
+                if (sg.partial) {
+#pragma unroll
+                    for (int k = 0; k < 32; ++k)
+                        if (i0 + k < w.I)
+                            __stcg(slot + (i0 + k) * 128, __uint_as_float(r[k]));
+                    continue;
+                }
+                if (i0 >= w.I)
+                    continue;
+                if constexpr (SILU) {
+                    // da transposed through the staging buffer, then row by row
+#pragma unroll
+                    for (int k = 0; k < 32; ++k)
+                        words[k * 32 + lane] = r[k];
+                    __syncwarp();
+#pragma unroll
+                    for (int t = 0; t < 4; ++t) {
+                        const int k = t * 8 + (lane >> 2), jg = lane & 3;
+                        const int i = i0 + k, j = j0 + jg * 8;
+                        if (i < w.I && j < w.J) {
+                            const int64_t o = static_cast<int64_t>(i) * 2 * w.J + j;
+                            uint4 g = ldg_nc_v4(gate_up + o), u = ldg_nc_v4(gate_up + o + w.J);
+                            uint4 a, b;
+                            read_pair(stage + k * 8 + jg * 2, k & 1, a, b);
+                            const float da[8] = {
+                                __uint_as_float(a.x), __uint_as_float(a.y), __uint_as_float(a.z),
+                                __uint_as_float(a.w), __uint_as_float(b.x), __uint_as_float(b.y),
+                                __uint_as_float(b.z), __uint_as_float(b.w)};
+                            silu_grad8(da, g, u, g, u);
+                            *reinterpret_cast<uint4 *>(out + o) = g;
+                            *reinterpret_cast<uint4 *>(out + o + w.J) = u;
+                        }
+                    }
+                } else {
+                    // rows 2p and 2p + 1 of a column in one word; the readers take them apart
+#pragma unroll
+                    for (int p = 0; p < 16; ++p)
+                        words[p * 32 + lane] =
+                            pack_bf16x2(__uint_as_float(r[2 * p]), __uint_as_float(r[2 * p + 1]));
+                    __syncwarp();
+#pragma unroll
+                    for (int t = 0; t < 2; ++t) {
+                        const int p = t * 8 + (lane >> 2), jg = lane & 3;
+                        const int i = i0 + 2 * p, j = j0 + jg * 8;
+                        uint4 a, b;
+                        read_pair(stage + p * 8 + jg * 2, p & 1, a, b);
+                        uint16_t *dst = out + static_cast<int64_t>(i) * w.J + j;
+                        if (i < w.I && j < w.J)
+                            *reinterpret_cast<uint4 *>(dst) = make_uint4(
+                                __byte_perm(a.x, a.y, 0x5410), __byte_perm(a.z, a.w, 0x5410),
+                                __byte_perm(b.x, b.y, 0x5410), __byte_perm(b.z, b.w, 0x5410));
+                        if (i + 1 < w.I && j < w.J)
+                            *reinterpret_cast<uint4 *>(dst + w.J) = make_uint4(
+                                __byte_perm(a.x, a.y, 0x7632), __byte_perm(a.z, a.w, 0x7632),
+                                __byte_perm(b.x, b.y, 0x7632), __byte_perm(b.z, b.w, 0x7632));
+                    }
+                }
+                __syncwarp();
+            }
+        }
+    } else {
+        // converters: group g takes every kNarrowGroups-th k-block, its warp of lane quarter q
+        // the columns j = 32 q .. 32 q + 31. Q's tile has rows r of 128 bytes, 16-byte pieces
+        // swizzled by the row (TMA's 128-byte swizzle), so ldmatrix's eight rows fill all banks.
+        pdl_wait();
+        const int group = (warp - kNarrowConvWarp0) >> 2, quarter = warp & 3;
+        const uint32_t src = (lane & 15) * 128 + (((2 * quarter + (lane >> 4)) ^ (lane & 7)) << 4);
+        const uint32_t dst = tmem_base + Cfg::kTmemB + (static_cast<uint32_t>(quarter * 32) << 16);
+        GradBlocks blk(w, cta, group);
+        for (uint32_t it = group; blk.ok; it += kNarrowGroups) {
+            const uint32_t qs = it % QSTAGES, s = it % STAGES;
+            if (!mbar_wait(bar_qfull + 8 * qs, (it / QSTAGES) & 1u, limit_ns))
+                break;
+            __syncwarp();
+            uint32_t m[4][4];
+            uint4 sc[4];
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+                ldmatrix_b8_trans_x2(sQ + qs * Cfg::kQBytes + g * 2048 + src, m[g]);
+                sc[g] = reinterpret_cast<const uint4 *>(smem + Cfg::kScOff +
+                                                        qs * Cfg::kScBytes)[g * 4 + (lane & 3)];
+            }
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(bar_qempty + 8 * qs);
+            if (!mbar_wait(bar_empty + 8 * s, ((it / STAGES) & 1u) ^ 1u, limit_ns))
+                break;
+            __syncwarp();
+            tc_fence_after();
+#pragma unroll
+            for (int h = 0; h < 2; ++h) { // 16 columns j each
+                uint32_t o[16];
+#pragma unroll
+                for (int g = 0; g < 4; ++g) {
+                    convert4_rows<F8>(m[g][2 * h], sc[g], o[4 * g], o[4 * g + 1]);
+                    convert4_rows<F8>(m[g][2 * h + 1], sc[g], o[4 * g + 2], o[4 * g + 3]);
+                }
+                tmem_st_16x256b_x4(dst + s * (kGradBR / 2) + (static_cast<uint32_t>(16 * h) << 16),
+                                   o);
+            }
+            tmem_st_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(bar_full + 8 * s);
+            blk.advance(w, kNarrowGroups);
+        }
+    }
+    __syncwarp();
+    if (warp == 1)
+        tmem_relinquish();
+    tc_fence_before(); // every MMA and load of the accumulators is done before they are freed
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 1)
+        tmem_dealloc(tmem_base, Cfg::kTmemCols);
+}
+
 // The whole of Q to scaled bf16 ahead of the product, [R, J]: 16 codes a thread and step.
 template <bool F8>
 __global__ void __launch_bounds__(256) grad_dequant_kernel(const uint8_t *__restrict__ q,
@@ -718,7 +1134,7 @@ __device__ __forceinline__ int split_owner(int64_t v, int64_t U, int pairs)
 }
 
 // Adds the partial tiles of the split tiles, in the order of the pairs, and finishes them: block
-// (x, y) takes 8 rows of remaining tile y.
+// (x, y) takes 2048 values of remaining tile y.
 template <bool SILU>
 __global__ void __launch_bounds__(256) grad_fixup_kernel(const GradWork w,
                                                          const float *__restrict__ part,
@@ -731,10 +1147,10 @@ __global__ void __launch_bounds__(256) grad_fixup_kernel(const GradWork w,
     const int t = blockIdx.y;
     int ib, jb;
     tile_coords(w.whole + t, w.ni, w.nj, w.group_i, ib, jb);
-    const int rl = blockIdx.x * 8 + (threadIdx.x >> 5);
-    const int row = ib * kGradTile + rl;
-    const int cl = (threadIdx.x & 31) * 8, col = jb * kGradTile + cl;
-    if (row >= w.I || col >= w.J)
+    const int at = (blockIdx.x * 256 + threadIdx.x) * 8;
+    const int rl = at / w.tile_j, cl = at - rl * w.tile_j;
+    const int row = ib * w.tile_i + rl, col = jb * w.tile_j + cl;
+    if (rl >= w.tile_i || row >= w.I || col >= w.J)
         return;
     const int64_t U = static_cast<int64_t>(w.rem) * w.kblocks;
     const int64_t u0 = static_cast<int64_t>(t) * w.kblocks;
@@ -749,16 +1165,16 @@ __global__ void __launch_bounds__(256) grad_fixup_kernel(const GradWork w,
     // Only the first pair can have begun in an earlier tile (its slot 1); the others' ranges begin
     // here. Four parts are in flight, added in order.
     const float4 *src = reinterpret_cast<const float4 *>(
-        part + (static_cast<int64_t>(p0) * 2 * kGradTile + rl) * kGradTile + cl);
-    constexpr int kSlot = kGradTile * kGradTile / 4;
+        part + static_cast<int64_t>(p0) * 2 * w.tile_i * w.tile_j + at);
+    const int slot_words = w.tile_i * w.tile_j / 4;
     const bool second = static_cast<int64_t>(p0) * U / w.rem_pairs < u0;
     for (int p = p0; p <= p1; p += 4) {
         float4 v[4][2];
 #pragma unroll
         for (int e = 0; e < 4; ++e)
             if (p + e <= p1) {
-                const float4 *at = src + static_cast<int64_t>(p + e - p0) * 2 * kSlot +
-                                   (second && p + e == p0 ? kSlot : 0);
+                const float4 *at = src + static_cast<int64_t>(p + e - p0) * 2 * slot_words +
+                                   (second && p + e == p0 ? slot_words : 0);
                 v[e][0] = __ldcs(at);
                 v[e][1] = __ldcs(at + 1);
             }

@@ -21,7 +21,8 @@ pytestmark = pytest.mark.gpu
 # the kernel dequantizes itself (fewer than 1024 of them) and that a pass before it does
 SHAPES = [(1, 8, 16), (1, 4096, 4096), (16, 6144, 512), (3, 72, 48), (64, 64, 64), (65, 56, 272),
           (300, 264, 528), (257, 1032, 4112), (2304, 512, 2304), (2304, 1024, 2304),
-          (1000, 2056, 1040), (129, 14336, 256), (1100, 264, 528), (1100, 8200, 272)]
+          (1000, 2056, 1040), (129, 14336, 256), (1100, 264, 528), (1100, 8200, 272),
+          (33, 4104, 4112), (100, 6144, 528), (128, 1000, 2064), (20, 640, 19072)]
 
 
 def _codes(shape, f8, seed):
@@ -168,7 +169,8 @@ def test_extreme_codes_and_zero_scales():
 
 @pytest.mark.parametrize("name,M,N,K", [("dgrad", 40, 4096, 512), ("wgrad", 2100, 264, 272),
                                         ("dgrad_silu", 40, 4096, 512),
-                                        ("dgrad_silu", 1100, 8200, 272)])
+                                        ("dgrad_silu", 1100, 8200, 272),
+                                        ("dgrad", 300, 4096, 512)])
 def test_repeatable_streams_and_graphs(name, M, N, K):
     """The same bits on every call (split sums included), on a side stream, with the caller's
     workspace, and from a captured call replayed on new inputs beside another capture."""

@@ -47,10 +47,13 @@ def test_host_checks(L, name):
 def test_workspace_sizes(L):
     d, wg = L.w8a8_gemm_dgrad_workspace_size, L.w8a8_gemm_wgrad_workspace_size
     tile = 2 * 256 * 256 * 4  # two partial tiles per CTA pair
+    narrow = 2 * 16 * 128 * 4  # and per CTA of the kernel for up to 16 rows
     assert d(1, 64, 256) == 0                       # one k-block: nothing to split
-    assert d(1, 1024, 256) == 4 * tile              # 16 k-blocks, four for each pair
+    assert d(16, 2048, 128) == 8 * narrow           # 32 k-blocks, four for each CTA
+    assert d(17, 2048, 128) == 16 * narrow          # of 32 rows
     assert d(4, 12, 64) == 0 and d(0, 64, 64) == 0  # refused shapes
-    assert d(1, 4096, 4096) == 74 * tile            # 16 tiles of 64 k-blocks on 148 SMs
+    assert d(1, 4096, 4096) == 148 * narrow         # 32 tiles of 64 k-blocks on 148 SMs
+    assert d(129, 4096, 256) == 16 * tile           # 64 k-blocks, four for each pair
     assert d(2048, 72, 4096) == 72 * 4096 * 2       # many rows: the bf16 weight
     assert wg(72, 4096, 4096) == 72 * 4096 * 2      # or the bf16 activations; short sums whole
     assert wg(4096, 256, 256) == 16 * tile
