@@ -691,7 +691,9 @@ template <int NT> struct NarrowCfg {
     static constexpr int kQOff = STAGES * kABytes;
     static constexpr int kScOff = kQOff + QSTAGES * kQBytes; // 16 bytes for four r's scales
     static constexpr int kScBytes = kGradBR / 4 * 16;
-    static constexpr int kOutOff = kScOff + QSTAGES * kScBytes; // 4 KB per epilogue warp
+    static constexpr int kAhead = 8;
+    static constexpr int kRawOff = kScOff + QSTAGES * kScBytes; // scales as they come
+    static constexpr int kOutOff = kRawOff + kAhead * kGradBR * 4; // 4 KB per epilogue warp
     static constexpr int kBarOff = kOutOff + 4 * 4096;
     // full[S], empty[S], qfull[QS], qempty[QS], tfull[2], tempty[2], tensor-memory slot
     static constexpr int kSmemBytes = kBarOff + (2 * STAGES + 2 * QSTAGES + 4) * 8 + 16 + 1024;
@@ -892,29 +894,45 @@ __global__ void __launch_bounds__(kNarrowThreads, 1)
                 drain_ring(bar_qempty, it, QSTAGES, limit_ns);
         }
     } else if (warp == 3) {
-        // the k-block's scales as convert4 takes them: lane l < 16 those of r = 4 l .. 4 l + 3
+        // the k-block's scales as convert4_rows takes them, lane l < 16 those of r = 4 l .. 4 l + 3,
+        // copied to shared memory kAhead k-blocks early
         pdl_wait();
-        float next[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-        auto fetch = [&](int kb) {
+        constexpr int kAhead = Cfg::kAhead;
+        const uint32_t raw = sbase + Cfg::kRawOff;
+        GradBlocks ahead(w, cta, 0), blk(w, cta, 0);
+        auto copy = [&](uint32_t slot) {
+            if (ahead.ok) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int r = kb * kGradBR + 4 * lane + e;
-                next[e] = lane < kGradBR / 4 && r < w.R ? __ldg(scale + r) : 0.0f;
+                for (int e = 0; e < 2; ++e) {
+                    const int r = ahead.kb * kGradBR + e * 32 + lane;
+                    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(
+                                     raw + slot * (kGradBR * 4) + (e * 32 + lane) * 4),
+                                 "l"(scale + (r < w.R ? r : 0)), "r"(r < w.R ? 4 : 0)
+                                 : "memory");
+                }
+                ahead.advance(w, 1);
             }
+            stage_load_commit();
         };
-        GradBlocks blk(w, cta, 0);
-        if (blk.ok)
-            fetch(blk.kb);
-        for (uint32_t it = 0; blk.ok; ++it) {
+        for (int u = 0; u < kAhead; ++u)
+            copy(u);
+        uint32_t s = 0, ph = 0, slot = 0;
+        for (; blk.ok; blk.advance(w, 1)) {
+            stage_load_wait<kAhead - 1>();
+            __syncwarp();
+            float4 f = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            if (lane < kGradBR / 4)
+                f = reinterpret_cast<const float4 *>(smem + Cfg::kRawOff)[slot * (kGradBR / 4) + lane];
+            __syncwarp();
+            copy(slot);
+            if (++slot == kAhead)
+                slot = 0;
             uint32_t hi[4], lo[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                split_scale(next[e], hi[e], lo[e]);
-            blk.advance(w, 1);
-            if (blk.ok)
-                fetch(blk.kb); // a k-block early
-            const uint32_t s = it % QSTAGES;
-            if (!mbar_wait(bar_qempty + 8 * s, ((it / QSTAGES) & 1u) ^ 1u, limit_ns))
+            split_scale(f.x, hi[0], lo[0]);
+            split_scale(f.y, hi[1], lo[1]);
+            split_scale(f.z, hi[2], lo[2]);
+            split_scale(f.w, hi[3], lo[3]);
+            if (!mbar_wait(bar_qempty + 8 * s, ph ^ 1u, limit_ns))
                 break;
             if (lane < kGradBR / 4)
                 reinterpret_cast<uint4 *>(smem + Cfg::kScOff + s * Cfg::kScBytes)[lane] =
@@ -923,7 +941,12 @@ __global__ void __launch_bounds__(kNarrowThreads, 1)
             __syncwarp();
             if (lane == 0)
                 mbar_arrive(bar_qfull + 8 * s);
+            if (++s == QSTAGES) {
+                s = 0;
+                ph ^= 1u;
+            }
         }
+        stage_load_wait<0>(); // no copy into this CTA's shared memory outlives it
     } else if (warp < kNarrowConvWarp0) {
         // epilogue: the warp's lanes are 32 columns j; the rows i in chunks of 32
         pdl_wait();
