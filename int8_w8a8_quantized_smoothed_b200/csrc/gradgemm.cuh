@@ -156,6 +156,20 @@ __device__ __forceinline__ uint64_t sw128_mnmajor_desc(uint32_t saddr)
     return d;
 }
 
+// A ring's stage and the parity of its current round, kept running: the single-thread roles are
+// chains of dependent instructions, and a remainder by the number of stages in each of them
+// (with addresses computed anew) made a k-block's issue take 650 cycles.
+template <int N> struct Ring {
+    uint32_t s = 0, ph = 0;
+    __device__ __forceinline__ void next()
+    {
+        if (++s == N) {
+            s = 0;
+            ph ^= 1u;
+        }
+    }
+};
+
 // mbar_wait for a barrier that the other CTA of the pair arrives on too: acquire at cluster scope.
 __device__ __forceinline__ bool mbar_wait_cluster(uint32_t bar, uint32_t parity, uint64_t limit_ns)
 {
@@ -357,7 +371,7 @@ __global__ void __launch_bounds__(GradCfg<CONV>::kThreads, 1)
     const uint32_t bar_tfull = bar_qempty + 8 * QSTAGES;  // both
     const uint32_t bar_tempty = bar_tfull + 16;           // used in the even CTA
     const uint32_t tslot = bar_tempty + 16;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const uint32_t rank = cluster_ctarank();
     const int pair = blockIdx.x >> 1;
 
@@ -390,85 +404,94 @@ __global__ void __launch_bounds__(GradCfg<CONV>::kThreads, 1)
     const uint32_t tmem_base =
         *reinterpret_cast<volatile uint32_t *>(smem + (tslot - sbase));
 
+    // The roles' loops run on all lanes of their warp, so that the compiler keeps their state in
+    // uniform registers; one lane issues.
     if (warp == 0) {
-        if (lane == 0) {
-            pdl_wait();
-            const uint32_t full0 = map_peer_smem(bar_full, 0);
-            uint32_t it = 0;
-            bool ok = true;
-            GradWalk walk(w, pair);
-            GradSegment sg;
-            while (ok && walk.next(w, sg)) {
-                int ib, jb;
-                tile_coords(sg.tile, w.ni, w.nj, w.group_i, ib, jb);
-                const int i0 = ib * kGradTile + static_cast<int>(rank) * 128;
-                for (int kb = sg.kb0; kb < sg.kb1; ++kb, ++it) {
-                    const uint32_t s = it % STAGES;
-                    if (!mbar_wait(bar_empty + 8 * s, ((it / STAGES) & 1u) ^ 1u, limit_ns)) {
-                        ok = false;
-                        break;
-                    }
+        pdl_wait();
+        const uint32_t full0 = map_peer_smem(bar_full, 0);
+        uint32_t it = 0;
+        bool ok = true;
+        Ring<STAGES> ring;
+        GradWalk walk(w, pair);
+        GradSegment sg;
+        while (ok && walk.next(w, sg)) {
+            int ib, jb;
+            tile_coords(sg.tile, w.ni, w.nj, w.group_i, ib, jb);
+            const int i0 = ib * kGradTile + static_cast<int>(rank) * 128;
+            const int j0 = jb * kGradTile + static_cast<int>(rank) * 128;
+            int r0 = sg.kb0 * kGradBR;
+            for (int n = sg.kb1 - sg.kb0; n > 0; --n, ++it, r0 += kGradBR) {
+                if (!mbar_wait(bar_empty + 8 * ring.s, ring.ph ^ 1u, limit_ns)) {
+                    ok = false;
+                    break;
+                }
+                if (lane == 0) {
+                    const uint32_t full = full0 + 8 * ring.s;
                     if (rank == 0)
-                        mbar_expect_tx(bar_full + 8 * s,
+                        mbar_expect_tx(bar_full + 8 * ring.s,
                                        2 * (Cfg::kABytes + (CONV ? 0 : Cfg::kBBytes)));
-                    const uint32_t dst = sA + s * Cfg::kABytes;
+                    const uint32_t dst = sA + ring.s * Cfg::kABytes;
                     if constexpr (WGRAD) {
-                        tma_load_2d_pair(dst, &tmA, full0 + 8 * s, i0, kb * kGradBR);
-                        tma_load_2d_pair(dst + 8192, &tmA, full0 + 8 * s, i0 + 64, kb * kGradBR);
+                        tma_load_2d_pair(dst, &tmA, full, i0, r0);
+                        tma_load_2d_pair(dst + 8192, &tmA, full, i0 + 64, r0);
                     } else {
-                        tma_load_2d_pair(dst, &tmA, full0 + 8 * s, kb * kGradBR, i0);
+                        tma_load_2d_pair(dst, &tmA, full, r0, i0);
                     }
                     if constexpr (!CONV) {
-                        const int j0 = jb * kGradTile + static_cast<int>(rank) * 128;
-                        const uint32_t b = sB + s * Cfg::kBBytes;
-                        tma_load_2d_pair(b, &tmQ, full0 + 8 * s, j0, kb * kGradBR);
-                        tma_load_2d_pair(b + 8192, &tmQ, full0 + 8 * s, j0 + 64, kb * kGradBR);
+                        const uint32_t b = sB + ring.s * Cfg::kBBytes;
+                        tma_load_2d_pair(b, &tmQ, full, j0, r0);
+                        tma_load_2d_pair(b + 8192, &tmQ, full, j0 + 64, r0);
                     }
                 }
+                __syncwarp();
+                ring.next();
             }
-            if (ok) // every stage released by the MMAs before this CTA may leave
-                drain_ring(bar_empty, it, STAGES, limit_ns);
-            pdl_launch_dependents();
         }
+        if (ok) // every stage released by the MMAs before this CTA may leave
+            drain_ring(bar_empty, it, STAGES, limit_ns);
+        if (lane == 0)
+            pdl_launch_dependents();
     } else if (warp == 1) {
-        if (lane == 0 && rank == 0) {
+        if (rank == 0) {
             constexpr uint32_t idesc = idesc_bf16(kGradTile, kGradTile, WGRAD, true);
             // stage 0's descriptors; a stage further on adds its bytes / 16 to the address field
             const uint64_t da = WGRAD ? sw128_mnmajor_desc(sA) : sw128_kmajor_desc(sA);
             const uint64_t db = sw128_mnmajor_desc(sB);
             constexpr uint32_t kStepA = (WGRAD ? 2048 : 32) / 16, kStepB = 2048 / 16;
-            uint32_t s = 0, ph = 0, seg = 0;
             bool ok = true;
+            Ring<STAGES> ring;
+            Ring<2> acc;
             GradWalk walk(w, pair);
             GradSegment sg;
             while (ok && walk.next(w, sg)) {
-                const uint32_t buf = seg & 1u, aph = (seg >> 1) & 1u;
-                ++seg;
-                if (!mbar_wait_cluster(bar_tempty + 8 * buf, aph ^ 1u, limit_ns))
+                if (!mbar_wait_cluster(bar_tempty + 8 * acc.s, acc.ph ^ 1u, limit_ns))
                     break;
                 tc_fence_after();
-                const uint32_t d = tmem_base + buf * kGradTile;
+                const uint32_t d = tmem_base + acc.s * kGradTile;
                 uint32_t accumulate = 0;
                 for (int n = sg.kb1 - sg.kb0; n > 0; --n) {
-                    if (!mbar_wait_cluster(bar_full + 8 * s, ph, limit_ns)) {
+                    if (!mbar_wait_cluster(bar_full + 8 * ring.s, ring.ph, limit_ns)) {
                         ok = false;
                         break;
                     }
                     tc_fence_after();
-                    const uint64_t a0 = da + s * (Cfg::kABytes / 16), b0 = db + s * (Cfg::kBBytes / 16);
+                    if (lane == 0) {
+                        const uint64_t a0 = da + ring.s * (Cfg::kABytes / 16);
+                        const uint64_t b0 = db + ring.s * (Cfg::kBBytes / 16);
 #pragma unroll
-                    for (int k = 0; k < kGradBR / 16; ++k) {
-                        umma_bf16_pair(d, a0 + k * kStepA, b0 + k * kStepB, idesc, accumulate);
-                        accumulate = 1;
+                        for (int k = 0; k < kGradBR / 16; ++k)
+                            umma_bf16_pair(d, a0 + k * kStepA, b0 + k * kStepB, idesc,
+                                           k > 0 ? 1u : accumulate);
+                        umma_commit_pair(bar_empty + 8 * ring.s, 0x3);
                     }
-                    umma_commit_pair(bar_empty + 8 * s, 0x3);
-                    if (++s == STAGES) {
-                        s = 0;
-                        ph ^= 1u;
-                    }
+                    __syncwarp();
+                    accumulate = 1;
+                    ring.next();
                 }
-                if (ok)
-                    umma_commit_pair(bar_tfull + 8 * buf, 0x3);
+                if (ok && lane == 0)
+                    umma_commit_pair(bar_tfull + 8 * acc.s, 0x3);
+                __syncwarp();
+                acc.next();
             }
         }
     } else if (warp >= 4 && warp < 8) {
@@ -574,29 +597,32 @@ __global__ void __launch_bounds__(GradCfg<CONV>::kThreads, 1)
                 mbar_arrive_cluster(tempty0 + 8 * buf); // the leader's accumulator is free
         }
     } else if (CONV && warp == 2) {
-        if (lane == 0) {
-            pdl_wait();
-            uint32_t it = 0;
-            bool ok = true;
-            GradWalk walk(w, pair);
-            GradSegment sg;
-            while (ok && walk.next(w, sg)) {
-                int ib, jb;
-                tile_coords(sg.tile, w.ni, w.nj, w.group_i, ib, jb);
-                const int j0 = jb * kGradTile + static_cast<int>(rank) * 128;
-                for (int kb = sg.kb0; kb < sg.kb1; ++kb, ++it) {
-                    const uint32_t s = it % QSTAGES;
-                    if (!mbar_wait(bar_qempty + 8 * s, ((it / QSTAGES) & 1u) ^ 1u, limit_ns)) {
-                        ok = false;
-                        break;
-                    }
-                    mbar_expect_tx(bar_qfull + 8 * s, Cfg::kQBytes);
-                    tma_load_2d(sQ + s * Cfg::kQBytes, &tmQ, bar_qfull + 8 * s, j0, kb * kGradBR);
+        pdl_wait();
+        uint32_t it = 0;
+        bool ok = true;
+        Ring<QSTAGES> ring;
+        GradWalk walk(w, pair);
+        GradSegment sg;
+        while (ok && walk.next(w, sg)) {
+            int ib, jb;
+            tile_coords(sg.tile, w.ni, w.nj, w.group_i, ib, jb);
+            const int j0 = jb * kGradTile + static_cast<int>(rank) * 128;
+            int r0 = sg.kb0 * kGradBR;
+            for (int n = sg.kb1 - sg.kb0; n > 0; --n, ++it, r0 += kGradBR) {
+                if (!mbar_wait(bar_qempty + 8 * ring.s, ring.ph ^ 1u, limit_ns)) {
+                    ok = false;
+                    break;
                 }
+                if (lane == 0) {
+                    mbar_expect_tx(bar_qfull + 8 * ring.s, Cfg::kQBytes);
+                    tma_load_2d(sQ + ring.s * Cfg::kQBytes, &tmQ, bar_qfull + 8 * ring.s, j0, r0);
+                }
+                __syncwarp();
+                ring.next();
             }
-            if (ok)
-                drain_ring(bar_qempty, it, QSTAGES, limit_ns);
         }
+        if (ok)
+            drain_ring(bar_qempty, it, QSTAGES, limit_ns);
     } else if (CONV && warp >= kGradConvWarp0) {
         // converters: group g (four warps) takes every kGradConvGroups-th k-block, so the waits,
         // loads and fences of several k-blocks overlap. Two threads share a row r of the
@@ -788,7 +814,7 @@ __global__ void __launch_bounds__(kNarrowThreads, 1)
     const uint32_t bar_tfull = bar_qempty + 8 * QSTAGES;
     const uint32_t bar_tempty = bar_tfull + 16;
     const uint32_t tslot = bar_tempty + 16;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const int cta = blockIdx.x;
 
     if (threadIdx.x == 0) {
@@ -818,81 +844,93 @@ __global__ void __launch_bounds__(kNarrowThreads, 1)
         *reinterpret_cast<volatile uint32_t *>(smem + (tslot - sbase));
 
     if (warp == 0) {
-        if (lane == 0) {
-            pdl_wait();
-            uint32_t it = 0;
-            bool ok = true;
-            GradWalk walk(w, cta);
-            GradSegment sg;
-            while (ok && walk.next(w, sg)) {
-                for (int kb = sg.kb0; kb < sg.kb1; ++kb, ++it) {
-                    const uint32_t s = it % STAGES;
-                    if (!mbar_wait(bar_empty + 8 * s, ((it / STAGES) & 1u) ^ 1u, limit_ns)) {
-                        ok = false;
-                        break;
-                    }
-                    mbar_expect_tx(bar_full + 8 * s, Cfg::kABytes);
-                    tma_load_2d(sA + s * Cfg::kABytes, &tmA, bar_full + 8 * s, kb * kGradBR, 0);
-                }
-            }
-            if (ok) // every stage released by the MMAs before this CTA may leave
-                drain_ring(bar_empty, it, STAGES, limit_ns);
-            pdl_launch_dependents();
-        }
-    } else if (warp == 1) {
-        if (lane == 0) {
-            constexpr uint32_t idesc = idesc_bf16(128, NT, false, false);
-            uint32_t it = 0, seg = 0;
-            bool ok = true;
-            GradWalk walk(w, cta);
-            GradSegment sg;
-            while (ok && walk.next(w, sg)) {
-                const uint32_t buf = seg & 1u, aph = (seg >> 1) & 1u;
-                ++seg;
-                if (!mbar_wait(bar_tempty + 8 * buf, aph ^ 1u, limit_ns))
+        pdl_wait();
+        uint32_t it = 0;
+        bool ok = true;
+        Ring<STAGES> ring;
+        GradWalk walk(w, cta);
+        GradSegment sg;
+        while (ok && walk.next(w, sg)) {
+            int r0 = sg.kb0 * kGradBR;
+            for (int n = sg.kb1 - sg.kb0; n > 0; --n, ++it, r0 += kGradBR) {
+                if (!mbar_wait(bar_empty + 8 * ring.s, ring.ph ^ 1u, limit_ns)) {
+                    ok = false;
                     break;
+                }
+                if (lane == 0) {
+                    mbar_expect_tx(bar_full + 8 * ring.s, Cfg::kABytes);
+                    tma_load_2d(sA + ring.s * Cfg::kABytes, &tmA, bar_full + 8 * ring.s, r0, 0);
+                }
+                __syncwarp();
+                ring.next();
+            }
+        }
+        if (ok) // every stage released by the MMAs before this CTA may leave
+            drain_ring(bar_empty, it, STAGES, limit_ns);
+        if (lane == 0)
+            pdl_launch_dependents();
+    } else if (warp == 1) {
+        constexpr uint32_t idesc = idesc_bf16(128, NT, false, false);
+        const uint64_t da = sw128_kmajor_desc(sA);
+        bool ok = true;
+        Ring<STAGES> ring;
+        Ring<2> acc;
+        GradWalk walk(w, cta);
+        GradSegment sg;
+        while (ok && walk.next(w, sg)) {
+            if (!mbar_wait(bar_tempty + 8 * acc.s, acc.ph ^ 1u, limit_ns))
+                break;
+            tc_fence_after();
+            const uint32_t d = tmem_base + acc.s * NT;
+            uint32_t accumulate = 0;
+            for (int n = sg.kb1 - sg.kb0; n > 0; --n) {
+                if (!mbar_wait(bar_full + 8 * ring.s, ring.ph, limit_ns)) {
+                    ok = false;
+                    break;
+                }
                 tc_fence_after();
-                for (int kb = sg.kb0; kb < sg.kb1; ++kb, ++it) {
-                    const uint32_t s = it % STAGES;
-                    if (!mbar_wait(bar_full + 8 * s, (it / STAGES) & 1u, limit_ns)) {
-                        ok = false;
-                        break;
-                    }
-                    tc_fence_after();
-                    const uint64_t a0 = sw128_kmajor_desc(sA + s * Cfg::kABytes);
-                    const uint32_t b0 = tmem_base + Cfg::kTmemB + s * (kGradBR / 2);
+                if (lane == 0) {
+                    const uint64_t a0 = da + ring.s * (Cfg::kABytes / 16);
+                    const uint32_t b0 = tmem_base + Cfg::kTmemB + ring.s * (kGradBR / 2);
 #pragma unroll
                     for (int k = 0; k < kGradBR / 16; ++k)
-                        umma_bf16_ts(tmem_base + buf * NT, b0 + k * 8, a0 + k * 2, idesc,
-                                     (kb > sg.kb0 || k > 0) ? 1u : 0u);
-                    umma_commit(bar_empty + 8 * s);
+                        umma_bf16_ts(d, b0 + k * 8, a0 + k * 2, idesc, k > 0 ? 1u : accumulate);
+                    umma_commit(bar_empty + 8 * ring.s);
                 }
-                if (ok)
-                    umma_commit(bar_tfull + 8 * buf);
+                __syncwarp();
+                accumulate = 1;
+                ring.next();
             }
+            if (ok && lane == 0)
+                umma_commit(bar_tfull + 8 * acc.s);
+            __syncwarp();
+            acc.next();
         }
     } else if (warp == 2) {
-        if (lane == 0) {
-            pdl_wait();
-            uint32_t it = 0;
-            bool ok = true;
-            GradWalk walk(w, cta);
-            GradSegment sg;
-            while (ok && walk.next(w, sg)) {
-                const int j0 = sg.tile * 128;
-                for (int kb = sg.kb0; kb < sg.kb1; ++kb, ++it) {
-                    const uint32_t s = it % QSTAGES;
-                    if (!mbar_wait(bar_qempty + 8 * s, ((it / QSTAGES) & 1u) ^ 1u, limit_ns)) {
-                        ok = false;
-                        break;
-                    }
-                    mbar_expect_tx(bar_qfull + 8 * s, Cfg::kQBytes);
-                    tma_load_2d(sQ + s * Cfg::kQBytes, &tmQ, bar_qfull + 8 * s, j0, kb * kGradBR);
+        pdl_wait();
+        uint32_t it = 0;
+        bool ok = true;
+        Ring<QSTAGES> ring;
+        GradWalk walk(w, cta);
+        GradSegment sg;
+        while (ok && walk.next(w, sg)) {
+            const int j0 = sg.tile * 128;
+            int r0 = sg.kb0 * kGradBR;
+            for (int n = sg.kb1 - sg.kb0; n > 0; --n, ++it, r0 += kGradBR) {
+                if (!mbar_wait(bar_qempty + 8 * ring.s, ring.ph ^ 1u, limit_ns)) {
+                    ok = false;
+                    break;
                 }
+                if (lane == 0) {
+                    mbar_expect_tx(bar_qfull + 8 * ring.s, Cfg::kQBytes);
+                    tma_load_2d(sQ + ring.s * Cfg::kQBytes, &tmQ, bar_qfull + 8 * ring.s, j0, r0);
+                }
+                __syncwarp();
+                ring.next();
             }
-            if (ok)
-                drain_ring(bar_qempty, it, QSTAGES, limit_ns);
         }
+        if (ok)
+            drain_ring(bar_qempty, it, QSTAGES, limit_ns);
     } else if (warp == 3) {
         // the k-block's scales as convert4_rows takes them, lane l < 16 those of r = 4 l .. 4 l + 3,
         // copied to shared memory kAhead k-blocks early
