@@ -703,9 +703,11 @@ __global__ void __launch_bounds__(GradCfg<CONV>::kThreads, 1)
 // store to tensor memory takes, so it is neither stored to shared memory again nor waited for by a
 // proxy fence. (With 256 rows this form is the slower one: an MMA whose first operand is in tensor
 // memory took 690 cycles a k-block where the pair's took 610.) The scales, which here vary along
-// a register's bytes, come from shared memory, prepared by a warp of their own.
+// a register's bytes, are prepared by each converter warp, two rows a lane, and handed round by
+// shuffles; a warp of its own that put them into shared memory was a chain of dependent steps
+// of 670 cycles a k-block, the pace of the whole kernel.
 
-// warps: 0 A producer, 1 MMA, 2 Q producer, 3 scales; 4 .. 7 epilogue; 8 .. 23 converters
+// warps: 0 A producer, 1 MMA, 2 Q producer; 4 .. 7 epilogue; 8 .. 23 converters
 constexpr int kNarrowThreads = 768;
 constexpr int kNarrowConvWarp0 = 8;
 constexpr int kNarrowGroups = 4; // groups of four converter warps, each on its own k-block
@@ -715,11 +717,7 @@ template <int NT> struct NarrowCfg {
     static constexpr int kABytes = NT * kGradBR * 2;
     static constexpr int kQBytes = 128 * kGradBR;
     static constexpr int kQOff = STAGES * kABytes;
-    static constexpr int kScOff = kQOff + QSTAGES * kQBytes; // 16 bytes for four r's scales
-    static constexpr int kScBytes = kGradBR / 4 * 16;
-    static constexpr int kAhead = 8;
-    static constexpr int kRawOff = kScOff + QSTAGES * kScBytes; // scales as they come
-    static constexpr int kOutOff = kRawOff + kAhead * kGradBR * 4; // 4 KB per epilogue warp
+    static constexpr int kOutOff = kQOff + QSTAGES * kQBytes; // 4 KB per epilogue warp
     static constexpr int kBarOff = kOutOff + 4 * 4096;
     // full[S], empty[S], qfull[QS], qempty[QS], tfull[2], tempty[2], tensor-memory slot
     static constexpr int kSmemBytes = kBarOff + (2 * STAGES + 2 * QSTAGES + 4) * 8 + 16 + 1024;
@@ -823,7 +821,7 @@ __global__ void __launch_bounds__(kNarrowThreads, 1)
             mbar_init(bar_empty + 8 * s, 1);
         }
         for (int s = 0; s < QSTAGES; ++s) {
-            mbar_init(bar_qfull + 8 * s, 2); // Q's bytes, the scales
+            mbar_init(bar_qfull + 8 * s, 1);
             mbar_init(bar_qempty + 8 * s, 4);
         }
         for (int b = 0; b < 2; ++b) {
@@ -931,61 +929,7 @@ __global__ void __launch_bounds__(kNarrowThreads, 1)
         }
         if (ok)
             drain_ring(bar_qempty, it, QSTAGES, limit_ns);
-    } else if (warp == 3) {
-        // the k-block's scales as convert4_rows takes them, lane l < 16 those of r = 4 l .. 4 l + 3,
-        // copied to shared memory kAhead k-blocks early
-        pdl_wait();
-        constexpr int kAhead = Cfg::kAhead;
-        const uint32_t raw = sbase + Cfg::kRawOff;
-        GradBlocks ahead(w, cta, 0), blk(w, cta, 0);
-        auto copy = [&](uint32_t slot) {
-            if (ahead.ok) {
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const int r = ahead.kb * kGradBR + e * 32 + lane;
-                    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(
-                                     raw + slot * (kGradBR * 4) + (e * 32 + lane) * 4),
-                                 "l"(scale + (r < w.R ? r : 0)), "r"(r < w.R ? 4 : 0)
-                                 : "memory");
-                }
-                ahead.advance(w, 1);
-            }
-            stage_load_commit();
-        };
-        for (int u = 0; u < kAhead; ++u)
-            copy(u);
-        uint32_t s = 0, ph = 0, slot = 0;
-        for (; blk.ok; blk.advance(w, 1)) {
-            stage_load_wait<kAhead - 1>();
-            __syncwarp();
-            float4 f = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-            if (lane < kGradBR / 4)
-                f = reinterpret_cast<const float4 *>(smem + Cfg::kRawOff)[slot * (kGradBR / 4) + lane];
-            __syncwarp();
-            copy(slot);
-            if (++slot == kAhead)
-                slot = 0;
-            uint32_t hi[4], lo[4];
-            split_scale(f.x, hi[0], lo[0]);
-            split_scale(f.y, hi[1], lo[1]);
-            split_scale(f.z, hi[2], lo[2]);
-            split_scale(f.w, hi[3], lo[3]);
-            if (!mbar_wait(bar_qempty + 8 * s, ph ^ 1u, limit_ns))
-                break;
-            if (lane < kGradBR / 4)
-                reinterpret_cast<uint4 *>(smem + Cfg::kScOff + s * Cfg::kScBytes)[lane] =
-                    make_uint4(__byte_perm(hi[0], hi[1], 0x7632), __byte_perm(hi[2], hi[3], 0x7632),
-                               __byte_perm(lo[0], lo[1], 0x7632), __byte_perm(lo[2], lo[3], 0x7632));
-            __syncwarp();
-            if (lane == 0)
-                mbar_arrive(bar_qfull + 8 * s);
-            if (++s == QSTAGES) {
-                s = 0;
-                ph ^= 1u;
-            }
-        }
-        stage_load_wait<0>(); // no copy into this CTA's shared memory outlives it
-    } else if (warp < kNarrowConvWarp0) {
+    } else if (warp >= 4 && warp < kNarrowConvWarp0) {
         // epilogue: the warp's lanes are 32 columns j; the rows i in chunks of 32
         pdl_wait();
         const int quarter = warp & 3;
@@ -1077,7 +1021,7 @@ __global__ void __launch_bounds__(kNarrowThreads, 1)
                 __syncwarp();
             }
         }
-    } else {
+    } else if (warp >= kNarrowConvWarp0) {
         // converters: group g takes every kNarrowGroups-th k-block, its warp of lane quarter q
         // the columns j = 32 q .. 32 q + 31. Q's tile has rows r of 128 bytes, 16-byte pieces
         // swizzled by the row (TMA's 128-byte swizzle), so ldmatrix's eight rows fill all banks.
@@ -1085,20 +1029,41 @@ __global__ void __launch_bounds__(kNarrowThreads, 1)
         const int group = (warp - kNarrowConvWarp0) >> 2, quarter = warp & 3;
         const uint32_t src = (lane & 15) * 128 + (((2 * quarter + (lane >> 4)) ^ (lane & 7)) << 4);
         const uint32_t dst = tmem_base + Cfg::kTmemB + (static_cast<uint32_t>(quarter * 32) << 16);
+        float s0 = 0.0f, s1 = 0.0f; // the scales of rows 2 lane, 2 lane + 1 of the next k-block
         GradBlocks blk(w, cta, group);
+        auto fetch = [&]() {
+            if (blk.ok) {
+                const int r = blk.kb * kGradBR + 2 * lane;
+                s0 = r < w.R ? __ldg(scale + r) : 0.0f;
+                s1 = r + 1 < w.R ? __ldg(scale + r + 1) : 0.0f;
+            }
+        };
+        fetch();
         for (uint32_t it = group; blk.ok; it += kNarrowGroups) {
             const uint32_t qs = it % QSTAGES, s = it % STAGES;
+            uint32_t h0, h1, l0, l1;
+            split_scale(s0, h0, l0);
+            split_scale(s1, h1, l1);
+            h0 = __byte_perm(h0, h1, 0x7632);
+            l0 = __byte_perm(l0, l1, 0x7632);
+            uint4 sc[4];
+#pragma unroll
+            for (int g = 0; g < 4; ++g) { // rows 16 g + 4 (lane % 4) .. + 3
+                const int from = 8 * g + 2 * (lane & 3);
+                sc[g] = make_uint4(__shfl_sync(0xffffffffu, h0, from),
+                                   __shfl_sync(0xffffffffu, h0, from + 1),
+                                   __shfl_sync(0xffffffffu, l0, from),
+                                   __shfl_sync(0xffffffffu, l0, from + 1));
+            }
+            blk.advance(w, kNarrowGroups);
+            fetch(); // the group's next k-block's, in flight while this one is converted
             if (!mbar_wait(bar_qfull + 8 * qs, (it / QSTAGES) & 1u, limit_ns))
                 break;
             __syncwarp();
             uint32_t m[4][4];
-            uint4 sc[4];
 #pragma unroll
-            for (int g = 0; g < 4; ++g) {
+            for (int g = 0; g < 4; ++g)
                 ldmatrix_b8_trans_x2(sQ + qs * Cfg::kQBytes + g * 2048 + src, m[g]);
-                sc[g] = reinterpret_cast<const uint4 *>(smem + Cfg::kScOff +
-                                                        qs * Cfg::kScBytes)[g * 4 + (lane & 3)];
-            }
             __syncwarp();
             if (lane == 0)
                 mbar_arrive(bar_qempty + 8 * qs);
@@ -1122,7 +1087,6 @@ __global__ void __launch_bounds__(kNarrowThreads, 1)
             __syncwarp();
             if (lane == 0)
                 mbar_arrive(bar_full + 8 * s);
-            blk.advance(w, kNarrowGroups);
         }
     }
     __syncwarp();
