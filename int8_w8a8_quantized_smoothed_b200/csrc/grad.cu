@@ -214,7 +214,8 @@ bool grad_plan(int64_t I, int64_t J, int64_t R, bool wgrad, int sms, GradPlan *p
     w->tile_i = narrow ? p->nt : kGradTile;
     w->tile_j = narrow ? 128 : kGradTile;
     const int64_t ni = (I + w->tile_i - 1) / w->tile_i, nj = (J + w->tile_j - 1) / w->tile_j;
-    const int64_t tiles = ni * nj, kb = (R + kGradBR - 1) / kGradBR;
+    const int64_t br = narrow ? kNarrowBR : kGradBR;
+    const int64_t tiles = ni * nj, kb = (R + br - 1) / br;
     const int64_t pairs = narrow ? sms : sms / 2;
     if (tiles > (1 << 30))
         return false;
@@ -231,11 +232,12 @@ bool grad_plan(int64_t I, int64_t J, int64_t R, bool wgrad, int sms, GradPlan *p
     w->rem_pairs = w->rem;
     if (w->rem > 0) {
         // The last tiles' k-blocks are split over all pairs (CTAs) where that saves more time
-        // than the partial tiles cost: a k-block takes about 0.2 us (narrow), 0.55 us (converted
+        // than the partial tiles cost: a k-block takes about 0.4 us (narrow), 0.55 us (converted
         // by the kernel) or 0.35 us; the second launch about 4 us, storing and adding partial
         // tiles up to 8 us (by their rows).
-        const int64_t split = std::min(pairs, std::max<int64_t>(w->rem, w->rem * kb / 4));
-        const double each = narrow ? 0.2 : p->form == kGradConv ? 0.55 : 0.35;
+        const int64_t split =
+            std::min(pairs, std::max<int64_t>(w->rem, w->rem * kb / (narrow ? 2 : 4)));
+        const double each = narrow ? 0.4 : p->form == kGradConv ? 0.55 : 0.35;
         const double saved = each * (kb - static_cast<double>(w->rem * kb) / split);
         if (saved > 4.0 + (narrow ? 0.0 : 8.0 * std::min<int64_t>(I, kGradTile) / kGradTile))
             w->rem_pairs = static_cast<int>(split);
@@ -374,7 +376,8 @@ int grad_impl(bool f8, const uint16_t *dy, const void *q, const float *scale, in
     if (encode_grad(&ta, dy, M, N, 2, WGRAD ? kGradBR : box_i, true))
         return W8A8_ERR_CUDA;
     if (p.form != kGradDequant) {
-        if (encode_grad(&tq, q, R, K, 1, kGradBR, p.form == kGradNarrow))
+        if (encode_grad(&tq, q, R, K, 1, p.form == kGradNarrow ? kNarrowBR : kGradBR,
+                        p.form == kGradNarrow))
             return W8A8_ERR_CUDA;
         if constexpr (!WGRAD)
             if (p.form == kGradNarrow)

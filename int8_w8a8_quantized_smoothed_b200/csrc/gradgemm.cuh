@@ -102,6 +102,11 @@ struct GradBlocks {
 template <bool CONV> struct GradCfg {
     static constexpr int STAGES = CONV ? 5 : 6;
     static constexpr int QSTAGES = CONV ? 4 : 0;
+    // A converter group meets a stage of Q again only after it has used it before (see the narrow
+    // kernel's). Of the other ring it may meet one that another group used: it comes there having
+    // finished the k-block kGradConvGroups before, so the MMAs of STAGES k-blocks before that one,
+    // and of all earlier ones, are done, and it cannot be two rounds early.
+    static_assert(QSTAGES % kGradConvGroups == 0 && STAGES >= kGradConvGroups, "rings and groups");
     static constexpr int kThreads = CONV ? kGradThreads : 256; // without: no converter warps
     static constexpr int kABytes = 128 * kGradBR * 2;
     static constexpr int kBBytes = 128 * kGradBR * 2;
@@ -711,11 +716,18 @@ __global__ void __launch_bounds__(GradCfg<CONV>::kThreads, 1)
 constexpr int kNarrowThreads = 768;
 constexpr int kNarrowConvWarp0 = 8;
 constexpr int kNarrowGroups = 4; // groups of four converter warps, each on its own k-block
+// r per k-block: twice the pair kernel's, as the MMA's issue (wait, instructions, commit: about
+// 550 cycles with 64) was the pace
+constexpr int kNarrowBR = 128;
 
 template <int NT> struct NarrowCfg {
-    static constexpr int STAGES = 8, QSTAGES = NT == 128 ? 8 : 10;
-    static constexpr int kABytes = NT * kGradBR * 2;
-    static constexpr int kQBytes = 128 * kGradBR;
+    static constexpr int STAGES = 4, QSTAGES = NT == 128 ? 4 : 8;
+    // A converter group meets a stage of either ring again only after it has used it before: with
+    // other numbers it could come to a stage of Q a whole round early, while another group still
+    // waits for the load before it, and take that wait's parity for its own.
+    static_assert(STAGES % kNarrowGroups == 0 && QSTAGES % kNarrowGroups == 0, "rings and groups");
+    static constexpr int kABytes = NT * kNarrowBR * 2; // two swizzled tiles of 64 r
+    static constexpr int kQBytes = 128 * kNarrowBR;
     static constexpr int kQOff = STAGES * kABytes;
     static constexpr int kOutOff = kQOff + QSTAGES * kQBytes; // 4 KB per epilogue warp
     static constexpr int kBarOff = kOutOff + 4 * 4096;
@@ -725,7 +737,7 @@ template <int NT> struct NarrowCfg {
     // two accumulators of 128 lanes j x NT columns i, then the converted operand's stages
     static constexpr int kTmemCols = 512;
     static constexpr int kTmemB = 256;
-    static_assert(2 * NT <= kTmemB && kTmemB + STAGES * kGradBR / 2 <= kTmemCols, "tensor memory");
+    static_assert(2 * NT <= kTmemB && kTmemB + STAGES * kNarrowBR / 2 <= kTmemCols, "tensor memory");
 };
 
 // D (+)= A B^T with A in tensor memory and B in shared memory, bf16.
@@ -849,15 +861,17 @@ __global__ void __launch_bounds__(kNarrowThreads, 1)
         GradWalk walk(w, cta);
         GradSegment sg;
         while (ok && walk.next(w, sg)) {
-            int r0 = sg.kb0 * kGradBR;
-            for (int n = sg.kb1 - sg.kb0; n > 0; --n, ++it, r0 += kGradBR) {
+            int r0 = sg.kb0 * kNarrowBR;
+            for (int n = sg.kb1 - sg.kb0; n > 0; --n, ++it, r0 += kNarrowBR) {
                 if (!mbar_wait(bar_empty + 8 * ring.s, ring.ph ^ 1u, limit_ns)) {
                     ok = false;
                     break;
                 }
                 if (lane == 0) {
                     mbar_expect_tx(bar_full + 8 * ring.s, Cfg::kABytes);
-                    tma_load_2d(sA + ring.s * Cfg::kABytes, &tmA, bar_full + 8 * ring.s, r0, 0);
+                    const uint32_t dst = sA + ring.s * Cfg::kABytes;
+                    tma_load_2d(dst, &tmA, bar_full + 8 * ring.s, r0, 0);
+                    tma_load_2d(dst + Cfg::kABytes / 2, &tmA, bar_full + 8 * ring.s, r0 + 64, 0);
                 }
                 __syncwarp();
                 ring.next();
@@ -889,10 +903,12 @@ __global__ void __launch_bounds__(kNarrowThreads, 1)
                 tc_fence_after();
                 if (lane == 0) {
                     const uint64_t a0 = da + ring.s * (Cfg::kABytes / 16);
-                    const uint32_t b0 = tmem_base + Cfg::kTmemB + ring.s * (kGradBR / 2);
+                    const uint32_t b0 = tmem_base + Cfg::kTmemB + ring.s * (kNarrowBR / 2);
 #pragma unroll
-                    for (int k = 0; k < kGradBR / 16; ++k)
-                        umma_bf16_ts(d, b0 + k * 8, a0 + k * 2, idesc, k > 0 ? 1u : accumulate);
+                    for (int k = 0; k < kNarrowBR / 16; ++k)
+                        umma_bf16_ts(d, b0 + k * 8,
+                                     a0 + (k >> 2) * (Cfg::kABytes / 32) + (k & 3) * 2, idesc,
+                                     k > 0 ? 1u : accumulate);
                     umma_commit(bar_empty + 8 * ring.s);
                 }
                 __syncwarp();
@@ -913,8 +929,8 @@ __global__ void __launch_bounds__(kNarrowThreads, 1)
         GradSegment sg;
         while (ok && walk.next(w, sg)) {
             const int j0 = sg.tile * 128;
-            int r0 = sg.kb0 * kGradBR;
-            for (int n = sg.kb1 - sg.kb0; n > 0; --n, ++it, r0 += kGradBR) {
+            int r0 = sg.kb0 * kNarrowBR;
+            for (int n = sg.kb1 - sg.kb0; n > 0; --n, ++it, r0 += kNarrowBR) {
                 if (!mbar_wait(bar_qempty + 8 * ring.s, ring.ph ^ 1u, limit_ns)) {
                     ok = false;
                     break;
@@ -1029,59 +1045,70 @@ __global__ void __launch_bounds__(kNarrowThreads, 1)
         const int group = (warp - kNarrowConvWarp0) >> 2, quarter = warp & 3;
         const uint32_t src = (lane & 15) * 128 + (((2 * quarter + (lane >> 4)) ^ (lane & 7)) << 4);
         const uint32_t dst = tmem_base + Cfg::kTmemB + (static_cast<uint32_t>(quarter * 32) << 16);
-        float s0 = 0.0f, s1 = 0.0f; // the scales of rows 2 lane, 2 lane + 1 of the next k-block
+        float next[4] = {0.0f, 0.0f, 0.0f, 0.0f}; // rows 4 lane .. + 3 of the next k-block
         GradBlocks blk(w, cta, group);
         auto fetch = [&]() {
             if (blk.ok) {
-                const int r = blk.kb * kGradBR + 2 * lane;
-                s0 = r < w.R ? __ldg(scale + r) : 0.0f;
-                s1 = r + 1 < w.R ? __ldg(scale + r + 1) : 0.0f;
+                const int r = blk.kb * kNarrowBR + 4 * lane;
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    next[e] = r + e < w.R ? __ldg(scale + r + e) : 0.0f;
             }
         };
         fetch();
         for (uint32_t it = group; blk.ok; it += kNarrowGroups) {
             const uint32_t qs = it % QSTAGES, s = it % STAGES;
-            uint32_t h0, h1, l0, l1;
-            split_scale(s0, h0, l0);
-            split_scale(s1, h1, l1);
-            h0 = __byte_perm(h0, h1, 0x7632);
-            l0 = __byte_perm(l0, l1, 0x7632);
-            uint4 sc[4];
+            uint32_t hi[4], lo[4];
 #pragma unroll
-            for (int g = 0; g < 4; ++g) { // rows 16 g + 4 (lane % 4) .. + 3
-                const int from = 8 * g + 2 * (lane & 3);
-                sc[g] = make_uint4(__shfl_sync(0xffffffffu, h0, from),
-                                   __shfl_sync(0xffffffffu, h0, from + 1),
-                                   __shfl_sync(0xffffffffu, l0, from),
-                                   __shfl_sync(0xffffffffu, l0, from + 1));
-            }
+            for (int e = 0; e < 4; ++e)
+                split_scale(next[e], hi[e], lo[e]);
+            const uint4 own = make_uint4(
+                __byte_perm(hi[0], hi[1], 0x7632), __byte_perm(hi[2], hi[3], 0x7632),
+                __byte_perm(lo[0], lo[1], 0x7632), __byte_perm(lo[2], lo[3], 0x7632));
             blk.advance(w, kNarrowGroups);
             fetch(); // the group's next k-block's, in flight while this one is converted
             if (!mbar_wait(bar_qfull + 8 * qs, (it / QSTAGES) & 1u, limit_ns))
                 break;
             __syncwarp();
-            uint32_t m[4][4];
+            const uint32_t tile = sQ + qs * Cfg::kQBytes + src;
+            bool ok = true;
 #pragma unroll
-            for (int g = 0; g < 4; ++g)
-                ldmatrix_b8_trans_x2(sQ + qs * Cfg::kQBytes + g * 2048 + src, m[g]);
-            __syncwarp();
-            if (lane == 0)
-                mbar_arrive(bar_qempty + 8 * qs);
-            if (!mbar_wait(bar_empty + 8 * s, ((it / STAGES) & 1u) ^ 1u, limit_ns))
-                break;
-            __syncwarp();
-            tc_fence_after();
+            for (int half = 0; half < 2; ++half) { // 64 rows r each
+                uint32_t m[4][4];
 #pragma unroll
-            for (int h = 0; h < 2; ++h) { // 16 columns j each
-                uint32_t o[16];
+                for (int g = 0; g < 4; ++g)
+                    ldmatrix_b8_trans_x2(tile + half * 8192 + g * 2048, m[g]);
+                if (half == 0)
+                    ok = mbar_wait(bar_empty + 8 * s, ((it / STAGES) & 1u) ^ 1u, limit_ns);
+                __syncwarp();
+                if (half == 1 && lane == 0)
+                    mbar_arrive(bar_qempty + 8 * qs);
+                tc_fence_after();
+                uint4 sc[4]; // rows 64 half + 16 g + 4 (lane % 4) .. + 3
 #pragma unroll
                 for (int g = 0; g < 4; ++g) {
-                    convert4_rows<F8>(m[g][2 * h], sc[g], o[4 * g], o[4 * g + 1]);
-                    convert4_rows<F8>(m[g][2 * h + 1], sc[g], o[4 * g + 2], o[4 * g + 3]);
+                    const int from = 16 * half + 4 * g + (lane & 3);
+                    sc[g] = make_uint4(__shfl_sync(0xffffffffu, own.x, from),
+                                       __shfl_sync(0xffffffffu, own.y, from),
+                                       __shfl_sync(0xffffffffu, own.z, from),
+                                       __shfl_sync(0xffffffffu, own.w, from));
                 }
-                tmem_st_16x256b_x4(dst + s * (kGradBR / 2) + (static_cast<uint32_t>(16 * h) << 16),
-                                   o);
+#pragma unroll
+                for (int c = 0; c < 2; ++c) { // 16 columns j each
+                    uint32_t o[16];
+#pragma unroll
+                    for (int g = 0; g < 4; ++g) {
+                        convert4_rows<F8>(m[g][2 * c], sc[g], o[4 * g], o[4 * g + 1]);
+                        convert4_rows<F8>(m[g][2 * c + 1], sc[g], o[4 * g + 2], o[4 * g + 3]);
+                    }
+                    if (ok)
+                        tmem_st_16x256b_x4(dst + s * (kNarrowBR / 2) + half * 32 +
+                                               (static_cast<uint32_t>(16 * c) << 16),
+                                           o);
+                }
             }
+            if (!ok)
+                break;
             tmem_st_wait();
             tc_fence_before();
             __syncwarp();

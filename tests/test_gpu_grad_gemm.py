@@ -217,6 +217,34 @@ def test_repeatable_streams_and_graphs(name, M, N, K):
     assert torch.equal(outs[0], first) and torch.equal(outs[1], other)
 
 
+@pytest.mark.parametrize("M,N,K", [(16, 28672, 4096), (128, 14336, 4096), (512, 8192, 4096),
+                                   (2048, 4096, 4096)])
+def test_many_calls_back_to_back(M, N, K):
+    """Long sums, one launch right after another (from a graph too): every form's load, convert
+    and multiply rings run full and out of step, and each call gives the first one's bits."""
+    dy, q, s = _dy(M, N, 40), _codes((N, K), False, 41), _scales(N, 42)
+    ref = w8.w8a8_gemm_dgrad(dy, q, s)
+    b = _dequantized(q, s)
+    want = dy.double() @ b
+    _assert_close(ref, want, _tol(want, dy.double().abs() @ b.abs(), N))
+    outs = [torch.empty_like(ref) for _ in range(25)]
+    for o in outs:
+        w8.w8a8_gemm_dgrad(dy, q, s, dx=o)
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, ref) for o in outs)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        for o in outs:
+            w8.w8a8_gemm_dgrad(dy, q, s, dx=o)
+    for _ in range(4):
+        for o in outs:
+            o.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(o, ref) for o in outs)
+    assert w8.w8a8_last_device_status() == 0
+
+
 def test_gradients_through_a_gated_block_match_the_formula():
     """The run a tuning step makes: forward codes by the row kernels and the GEMM, then the norms
     after the block, and every gradient back to the block's input and its weights."""
