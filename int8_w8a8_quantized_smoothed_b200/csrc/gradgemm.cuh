@@ -659,9 +659,6 @@ __global__ void __launch_bounds__(GradCfg<CONV>::kThreads, 1)
 #pragma unroll
             for (int k = 0; k < 4; ++k)
                 raw[k] = *reinterpret_cast<const uint4 *>(src + (((2 * k + half + lane) & 7) << 4));
-            __syncwarp();
-            if (lane == 0)
-                mbar_arrive(bar_qempty + 8 * qs);
             if (!mbar_wait(bar_empty + 8 * s, ((it / STAGES) & 1u) ^ 1u, limit_ns))
                 break;
             uint8_t *bt = smem + Cfg::kBOff + s * Cfg::kBBytes + row * 128;
@@ -679,8 +676,13 @@ __global__ void __launch_bounds__(GradCfg<CONV>::kThreads, 1)
             }
             fence_proxy_async_smem(); // the tensor cores read what was stored
             __syncwarp();
-            if (lane == 0)
+            if (lane == 0) {
                 mbar_arrive_cluster(full0 + 8 * s);
+                // Q's stage goes back only here: an arrival does not wait for loads in flight, and
+                // right after the loads (stores of other warps before them in the queue) the next
+                // bulk copy overwrote bytes not yet read, in one call of two hundred
+                mbar_arrive(bar_qempty + 8 * qs);
+            }
             // the scale of the group's next k-block, after the fence, which would wait for it
             blk.advance(w, kGradConvGroups);
             if (blk.ok)
@@ -1081,8 +1083,6 @@ __global__ void __launch_bounds__(kNarrowThreads, 1)
                 if (half == 0)
                     ok = mbar_wait(bar_empty + 8 * s, ((it / STAGES) & 1u) ^ 1u, limit_ns);
                 __syncwarp();
-                if (half == 1 && lane == 0)
-                    mbar_arrive(bar_qempty + 8 * qs);
                 tc_fence_after();
                 uint4 sc[4]; // rows 64 half + 16 g + 4 (lane % 4) .. + 3
 #pragma unroll
@@ -1112,8 +1112,10 @@ __global__ void __launch_bounds__(kNarrowThreads, 1)
             tmem_st_wait();
             tc_fence_before();
             __syncwarp();
-            if (lane == 0)
+            if (lane == 0) {
                 mbar_arrive(bar_full + 8 * s);
+                mbar_arrive(bar_qempty + 8 * qs); // not before the loads are done (see the pair's)
+            }
         }
     }
     __syncwarp();
