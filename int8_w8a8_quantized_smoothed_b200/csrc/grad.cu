@@ -126,42 +126,64 @@ int sandwich_quant_impl(const uint16_t *y, const uint16_t *residual, const float
 }
 
 // Backward launch shape: clusters of `csize` CTAs of `threads`, one vector of 8 columns per
-// thread; as many clusters as the device holds at 128 registers a thread, never more than rows.
+// thread, rings of three rows where two CTAs of 4096 columns (or one of 8192) leave the room, else
+// of two. As many clusters as the device holds at 64 registers a thread, but beyond one CTA an SM
+// only for at least four rows each, since each of them stores and adds sums as long as two rows.
 struct SandwichBackPlan {
-    int csize, threads;
+    int csize, threads, stages, smem;
     int64_t clusters;
-    size_t ws_bytes;
 };
 
-SandwichBackPlan sandwich_back_plan(int64_t M, int64_t K, int sms)
+SandwichBackPlan sandwich_back_plan(int64_t M, int64_t K, int arrays, int sms)
 {
+    constexpr int kSmemPerSm = 227 * 1024, kReserved = 1024;
     SandwichBackPlan p;
     const int64_t nvec = K / 8;
     p.csize = static_cast<int>((nvec + kBackMaxThreads - 1) / kBackMaxThreads);
     const int64_t per = (nvec + p.csize - 1) / p.csize;
     p.threads = static_cast<int>((per + 31) / 32 * 32);
-    const int64_t resident = static_cast<int64_t>(sms) * (kBackMaxThreads / p.threads) / p.csize;
-    p.clusters = std::max<int64_t>(1, std::min<int64_t>(M, resident));
-    p.ws_bytes = static_cast<size_t>(p.clusters) * 2 * static_cast<size_t>(K) * sizeof(float);
+    const int cols = static_cast<int>(per * 8);
+    const int by_threads = kBackMaxThreads / p.threads;
+    auto resident = [&](int stages) {
+        return std::min(by_threads, kSmemPerSm / (back_smem_bytes(cols, arrays, stages) + kReserved));
+    };
+    p.stages = resident(3) >= std::min(by_threads, 2) ? 3 : 2;
+    p.smem = back_smem_bytes(cols, arrays, p.stages);
+    const int per_sm = std::max(1, std::min(resident(p.stages), 8));
+    const int64_t one = std::max<int64_t>(1, sms / p.csize), all = sms * per_sm / p.csize;
+    p.clusters = std::min<int64_t>(M, std::max(one, std::min<int64_t>(all, M / 4)));
     return p;
 }
+
+// The workspace does not depend on which inputs a call has: the most clusters of any.
+size_t sandwich_back_ws(int64_t M, int64_t K, int sms)
+{
+    int64_t clusters = 0;
+    for (int arrays = 3; arrays <= 5; ++arrays)
+        clusters = std::max(clusters, sandwich_back_plan(M, K, arrays, sms).clusters);
+    return static_cast<size_t>(clusters) * 2 * static_cast<size_t>(K) * sizeof(float);
+}
+
+// The most that a plan takes (resident() >= 1), and that the widest rows fit with two stages.
+constexpr int kBackMaxSmem = 226 * 1024;
+static_assert(back_smem_bytes(8 * kBackMaxThreads, 5, 2) <= kBackMaxSmem, "shared memory per CTA");
 
 template <bool POST, int GATE>
 int launch_sandwich_back(const SandwichBack &a, const SandwichBackPlan &p, int dev, cudaStream_t st)
 {
     if (p.csize > 1) {
         const void *fn = reinterpret_cast<const void *>(&sandwich_back_kernel<POST, GATE, true>);
-        if (int rc = ensure_smem(fn, dev, 0))
+        if (int rc = ensure_smem(fn, dev, kBackMaxSmem))
             return rc;
         return launch_kernel_cluster(sandwich_back_kernel<POST, GATE, true>,
                                      dim3(static_cast<unsigned>(p.clusters * p.csize)),
-                                     dim3(p.threads), 0, st, static_cast<unsigned>(p.csize), a);
+                                     dim3(p.threads), p.smem, st, static_cast<unsigned>(p.csize), a);
     }
     const void *fn = reinterpret_cast<const void *>(&sandwich_back_kernel<POST, GATE, false>);
-    if (int rc = ensure_smem(fn, dev, 0))
+    if (int rc = ensure_smem(fn, dev, kBackMaxSmem))
         return rc;
     return launch_kernel(sandwich_back_kernel<POST, GATE, false>,
-                         dim3(static_cast<unsigned>(p.clusters)), dim3(p.threads), 0, st, a);
+                         dim3(static_cast<unsigned>(p.clusters)), dim3(p.threads), p.smem, st, a);
 }
 
 template <bool POST>
@@ -501,7 +523,7 @@ size_t w8a8_sandwich_rmsnorm_backward_workspace_size(int64_t M, int64_t K)
     int dev, sms = 148;
     if (current_device(&dev, &sms))
         sms = 148;
-    return sandwich_back_plan(M, K, sms).ws_bytes;
+    return sandwich_back_ws(M, K, sms);
 }
 
 int w8a8_sandwich_rmsnorm_backward(const w8a8_bf16 *dz, const w8a8_bf16 *dh, const w8a8_bf16 *y,
@@ -537,9 +559,10 @@ int w8a8_sandwich_rmsnorm_backward(const w8a8_bf16 *dz, const w8a8_bf16 *dh, con
     int dev, sms;
     if ((rc = current_device(&dev, &sms)))
         return rc;
-    const SandwichBackPlan p = sandwich_back_plan(M, K, sms);
-    if (workspace == nullptr || workspace_bytes < p.ws_bytes)
+    if (workspace == nullptr || workspace_bytes < sandwich_back_ws(M, K, sms))
         return W8A8_ERR_WORKSPACE;
+    const SandwichBackPlan p =
+        sandwich_back_plan(M, K, 3 + (dh ? 1 : 0) + (gate_kind == W8A8_GATE_FULL ? 1 : 0), sms);
     SandwichBack a;
     a.dz = dz;
     a.dh = dh;
@@ -558,6 +581,8 @@ int w8a8_sandwich_rmsnorm_backward(const w8a8_bf16 *dz, const w8a8_bf16 *dh, con
     a.eps_pre = eps;
     a.K = static_cast<int>(K);
     a.M = static_cast<int>(M);
+    a.stages = p.stages;
+    a.limit_ns = kWaitLimitNs;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     rc = gamma_post ? launch_sandwich_back_gate<true>(a, gate_kind, p, dev, st)
                     : launch_sandwich_back_gate<false>(a, gate_kind, p, dev, st);

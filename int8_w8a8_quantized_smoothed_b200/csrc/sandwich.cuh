@@ -144,15 +144,18 @@ __global__ void __launch_bounds__(NCH <= 2 ? 256 : 1024, NCH <= 2 ? 3 : 1)
 // S needs D, whose own sums are linear in it: sum p D = sum p dh + r2 sum p w - r2^3 A / K sum p h
 // (p with the gate where it varies along the row), so one round of row sums gives all of them.
 // dgamma_pre = sum_m dz h r2 and T = sum_m [gate] D y r1 are summed over the rows a CTA takes in
-// registers (each thread keeps its eight columns for every row); part_kernel adds the CTAs'
-// sums in a fixed order.
+// registers (each thread keeps its eight columns for every row); sandwich_part_kernel adds the
+// CTAs' sums in a fixed order.
 //
-// A CTA covers up to 4096 columns (512 threads, one vector of 8 each); wider rows take a cluster
-// of CTAs whose row sums meet through distributed shared memory, one barrier a row either way.
+// A CTA covers up to 8192 columns (1024 threads, one vector of 8 each); wider rows take a cluster
+// of CTAs whose row sums meet through distributed shared memory, one barrier a row either way. The
+// rows come by bulk copies into a ring of two or three in shared memory, so that the next rows'
+// bytes are on their way without a register held for them, and are read twice from there, before
+// and after the row's sums are known. (With the next row in registers, 512 threads and two CTAs a
+// row of 8192, 8192 x 8192 took 470 us, 7900 cycles a row.)
 
-constexpr int kBackMaxThreads = 512;
+constexpr int kBackMaxThreads = 1024;
 constexpr int kBackSums = 6; // h h, w h, y y, p dh, p w, p h
-
 struct SandwichBack {
     const uint16_t *dz, *dh, *y, *h;
     const float *gamma_post, *gamma_pre;
@@ -161,15 +164,36 @@ struct SandwichBack {
     float *dgate_tok;
     float *part; // [clusters][2][K]: dgamma_pre, T
     float res_scale, eps_post, eps_pre;
-    int K, M;
+    int K, M, stages;
+    unsigned long long limit_ns;
 };
 
-__device__ __forceinline__ float warp_sum_f(float v)
+// Shared memory of a CTA with `cols` columns: the ring, the warps' sums by row parity, the ring's
+// barriers.
+__host__ __device__ constexpr int back_smem_bytes(int cols, int arrays, int stages)
 {
+    return 2 * cols * arrays * stages + 2 * kBackSums * 32 * 4 + stages * 8;
+}
+
+// Sums of eight values over the warp: of value j, all lanes with (lane >> 2) == j hold it (by
+// exchanging halves of the values first, 9 shuffles instead of 5 for each).
+__device__ __forceinline__ float warp_sum8(const float (&v)[8], int lane)
+{
+    float a[4], b[2];
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1)
-        v += __shfl_xor_sync(0xffffffffu, v, o);
-    return v;
+    for (int i = 0; i < 4; ++i) {
+        const float keep = (lane & 16) ? v[4 + i] : v[i], send = (lane & 16) ? v[i] : v[4 + i];
+        a[i] = keep + __shfl_xor_sync(0xffffffffu, send, 16);
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const float keep = (lane & 8) ? a[2 + i] : a[i], send = (lane & 8) ? a[i] : a[2 + i];
+        b[i] = keep + __shfl_xor_sync(0xffffffffu, send, 8);
+    }
+    const float keep = (lane & 4) ? b[1] : b[0], send = (lane & 4) ? b[0] : b[1];
+    float c = keep + __shfl_xor_sync(0xffffffffu, send, 4);
+    c += __shfl_xor_sync(0xffffffffu, c, 2);
+    return c + __shfl_xor_sync(0xffffffffu, c, 1);
 }
 
 __device__ __forceinline__ float ld_dsmem_f32(uint32_t addr)
@@ -179,13 +203,17 @@ __device__ __forceinline__ float ld_dsmem_f32(uint32_t addr)
     return r;
 }
 
+// Columns 2e and 2e + 1 of a half vector's words.
+__device__ __forceinline__ float2 bf16_pair(const uint2 v, int e)
+{
+    const uint32_t w = e ? v.y : v.x;
+    return make_float2(bf16_lo(w), bf16_hi(w));
+}
+
 template <bool POST, int GATE, bool CLUSTER>
 __global__ void __launch_bounds__(kBackMaxThreads, 1) sandwich_back_kernel(const SandwichBack a)
 {
-    __shared__ float sh[2][kBackSums][16]; // by row parity: one barrier a row
-    if (threadIdx.x == 0)
-        pdl_launch_dependents();
-    pdl_wait();
+    extern __shared__ __align__(16) uint8_t back_smem[];
     const int K = a.K;
     const int nvec = K >> 3;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -196,153 +224,215 @@ __global__ void __launch_bounds__(kBackMaxThreads, 1) sandwich_back_kernel(const
         asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(csize));
     }
     const int cl = blockIdx.x / csize, ncl = gridDim.x / csize;
-    const int per = (nvec + csize - 1) / csize;
-    const int vi = rank * per + threadIdx.x;
-    const bool on = static_cast<int>(threadIdx.x) < per && vi < nvec;
-    const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
-    constexpr bool kSums = POST || GATE == kGateToken; // sums of p wanted
-    float gpost[8], gpre[8], gch[8];
+    const int per = (nvec + csize - 1) / csize; // vectors of a CTA; the last one may have fewer
+    const int v0 = rank * per;
+    const int have = min(per, nvec - v0);
+    const int vi = v0 + threadIdx.x;
+    const bool on = static_cast<int>(threadIdx.x) < have;
+    const bool has_dh = a.dh != nullptr;
+    const int arrays = 3 + (has_dh ? 1 : 0) + (GATE == kGateFull ? 1 : 0);
+    const int stage_vecs = arrays * per;
+    uint4 *ring = reinterpret_cast<uint4 *>(back_smem);
+    float(*sh)[kBackSums][32] =
+        reinterpret_cast<float(*)[kBackSums][32]>(ring + a.stages * stage_vecs);
+    const uint32_t bars = smem_u32(sh + 2);
+
+    if (threadIdx.x == 0) {
+        pdl_launch_dependents();
+        for (int s = 0; s < a.stages; ++s)
+            mbar_init(bars + 8 * s, 1);
+        fence_mbar_init();
+    }
+    __syncthreads();
+    pdl_wait();
+    auto fetch = [&](int64_t row, int s) { // one thread
+        const uint32_t bytes = static_cast<uint32_t>(have) * 16;
+        const uint32_t bar = bars + 8 * s;
+        const int64_t at = row * nvec + v0;
+        uint32_t dst = smem_u32(ring + s * stage_vecs);
+        mbar_expect_tx(bar, bytes * arrays);
+        auto copy = [&](const void *p) {
+            bulk_load_g2s(dst, static_cast<const uint4 *>(p) + at, bytes, bar);
+            dst += per * 16;
+        };
+        copy(a.dz);
+        copy(a.y);
+        copy(a.h);
+        if (has_dh)
+            copy(a.dh);
+        if constexpr (GATE == kGateFull)
+            copy(a.gate);
+    };
+    if (threadIdx.x == 0)
+        for (int s = 0; s < a.stages; ++s)
+            if (cl + static_cast<int64_t>(s) * ncl < a.M)
+                fetch(cl + static_cast<int64_t>(s) * ncl, s);
+    // gamma_smoothed, and gamma_post with the channel gate where there is one
+    float gp[8], gq[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-        gpost[i] = gpre[i] = gch[i] = 1.0f;
+        gp[i] = gq[i] = 1.0f;
     if (on) {
-        load8_f32(a.gamma_pre, vi, gpre);
+        load8_f32(a.gamma_pre, vi, gp);
         if constexpr (POST)
-            load8_f32(a.gamma_post, vi, gpost);
-        if constexpr (GATE == kGateChannel)
-            load8_f32(static_cast<const float *>(a.gate), vi, gch);
+            load8_f32(a.gamma_post, vi, gq);
+        if constexpr (GATE == kGateChannel) {
+            float g[8];
+            load8_f32(static_cast<const float *>(a.gate), vi, g);
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                gq[i] *= g[i];
+        }
     }
+    constexpr bool kSums = POST || GATE == kGateToken; // sums of p wanted
+    constexpr bool kT = POST || GATE == kGateChannel;
     float acc_pre[8], acc_t[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i)
         acc_pre[i] = acc_t[i] = 0.0f;
-    uint4 ndz = zero, ndh = zero, ny = zero, nh = zero, ng = zero;
-    auto fetch = [&](int64_t row) {
-        if (on && row < a.M) {
-            const int64_t o = row * nvec + vi;
-            ndz = ldg_nc_v4(reinterpret_cast<const uint4 *>(a.dz) + o);
-            if (a.dh)
-                ndh = reinterpret_cast<const uint4 *>(a.dh)[o]; // dres may be dh: a plain load
-            ny = ldg_nc_v4(reinterpret_cast<const uint4 *>(a.y) + o);
-            nh = ldg_nc_v4(reinterpret_cast<const uint4 *>(a.h) + o);
-            if constexpr (GATE == kGateFull)
-                ng = ldg_nc_v4(reinterpret_cast<const uint4 *>(a.gate) + o);
-        }
-    };
-    fetch(cl);
     const float invK = 1.0f / static_cast<float>(K);
-    uint32_t it = 0;
-    for (int64_t row = cl; row < a.M; row += ncl, ++it) {
-        float dz[8], D[8], y[8], h[8], g[8];
-        unpack8(ndz, dz);
-        unpack8(ndh, D);
-        unpack8(ny, y);
-        unpack8(nh, h);
-        if constexpr (GATE == kGateFull)
-            unpack8(ng, g);
-        else
+    int s = 0;
+    uint32_t ph = 0, parity = 0;
+    for (int64_t row = cl; row < a.M; row += ncl, parity ^= 1u) {
+        // a wait that ran out has raised the status word; the row is then worked on as it is
+        (void)mbar_wait(bars + 8 * s, ph, a.limit_ns);
+        const uint2 *st = reinterpret_cast<const uint2 *>(ring + s * stage_vecs + threadIdx.x);
+        const int next = 2 * per; // from one array to the next
+        float sum[8];
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-                g[i] = gch[i];
-        float gt = 1.0f;
-        if constexpr (GATE == kGateToken)
-            gt = a.gate ? __ldg(static_cast<const float *>(a.gate) + row) : 1.0f;
-        fetch(row + ncl);
-        float s[kBackSums];
+        for (int j = 0; j < 8; ++j)
+            sum[j] = 0.0f;
+        if (on) {
 #pragma unroll
-        for (int j = 0; j < kBackSums; ++j)
-            s[j] = 0.0f;
+            for (int hv = 0; hv < 2; ++hv) { // four columns at a time
+                const uint2 dz = st[hv], y = st[next + hv], h = st[2 * next + hv];
+                const uint2 dh = has_dh ? st[3 * next + hv] : make_uint2(0u, 0u);
+                uint2 g = make_uint2(0u, 0u);
+                if constexpr (GATE == kGateFull)
+                    g = st[(arrays - 1) * next + hv];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const float w = dz[i] * gpre[i];
-            s[0] = fmaf(h[i], h[i], s[0]);
-            s[1] = fmaf(w, h[i], s[1]);
-            if constexpr (POST)
-                s[2] = fmaf(y[i], y[i], s[2]);
-            if constexpr (kSums) {
-                const float p = GATE == kGateToken ? gpost[i] * y[i] : g[i] * gpost[i] * y[i];
-                s[3] = fmaf(p, D[i], s[3]);
-                s[4] = fmaf(p, w, s[4]);
-                s[5] = fmaf(p, h[i], s[5]);
+                for (int e = 0; e < 2; ++e) {
+                    const float2 dz2 = bf16_pair(dz, e), y2 = bf16_pair(y, e), h2 = bf16_pair(h, e);
+                    const float2 dh2 = bf16_pair(dh, e), g2 = bf16_pair(g, e);
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        const int i = 4 * hv + 2 * e + c;
+                        const float hh = c ? h2.y : h2.x, yy = c ? y2.y : y2.x;
+                        const float w = (c ? dz2.y : dz2.x) * gp[i];
+                        sum[0] = fmaf(hh, hh, sum[0]);
+                        sum[1] = fmaf(w, hh, sum[1]);
+                        if constexpr (POST)
+                            sum[2] = fmaf(yy, yy, sum[2]);
+                        if constexpr (kSums) {
+                            float p = gq[i] * yy;
+                            if constexpr (GATE == kGateFull)
+                                p *= c ? g2.y : g2.x;
+                            sum[3] = fmaf(p, c ? dh2.y : dh2.x, sum[3]);
+                            sum[4] = fmaf(p, w, sum[4]);
+                            sum[5] = fmaf(p, hh, sum[5]);
+                        }
+                    }
+                }
             }
         }
-        float(&buf)[kBackSums][16] = sh[it & 1];
-#pragma unroll
-        for (int j = 0; j < kBackSums; ++j) {
-            if ((j == 2 && !POST) || (j > 2 && !kSums))
-                continue;
-            s[j] = warp_sum_f(s[j]);
-            if (lane == 0)
-                buf[j][warp] = s[j];
-        }
+        float(&buf)[kBackSums][32] = sh[parity];
+        const float mine = warp_sum8(sum, lane);
+        if ((lane & 3) == 0 && (lane >> 2) < kBackSums)
+            buf[lane >> 2][warp] = mine;
         if constexpr (CLUSTER)
             cluster_sync();
         else
             __syncthreads();
-#pragma unroll
-        for (int j = 0; j < kBackSums; ++j) {
-            if ((j == 2 && !POST) || (j > 2 && !kSums))
-                continue;
-            float t = 0.0f;
-            if constexpr (CLUSTER) {
-                for (uint32_t r = 0; r < csize; ++r)
-                    if (lane < nw)
-                        t += ld_dsmem_f32(map_peer_smem(smem_u32(&buf[j][lane]), r));
-            } else {
-                t = lane < nw ? buf[j][lane] : 0.0f;
-            }
-            s[j] = warp_sum_f(t);
+        // every thread has used what it read of the row before this one: its stage is free
+        if (threadIdx.x == 0 && row != cl) {
+            const int64_t ahead = row + static_cast<int64_t>(a.stages - 1) * ncl;
+            if (ahead < a.M)
+                fetch(ahead, s == 0 ? a.stages - 1 : s - 1);
         }
-        const float r2 = 1.0f / sqrtf(fmaf(s[0], invK, a.eps_pre));
-        const float c2 = r2 * r2 * r2 * (s[1] * invK);
-        const float r1 = POST ? 1.0f / sqrtf(fmaf(s[2], invK, a.eps_post)) : 1.0f;
-        const float sp = fmaf(-c2, s[5], fmaf(r2, s[4], s[3])); // sum p D
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            sum[j] = 0.0f;
+        if (lane < nw) {
+#pragma unroll
+            for (int j = 0; j < kBackSums; ++j) {
+                if constexpr (CLUSTER) {
+                    for (uint32_t r = 0; r < csize; ++r)
+                        sum[j] += ld_dsmem_f32(map_peer_smem(smem_u32(&buf[j][lane]), r));
+                } else {
+                    sum[j] = buf[j][lane];
+                }
+            }
+        }
+        const float all = warp_sum8(sum, lane);
+        float t[kBackSums];
+#pragma unroll
+        for (int j = 0; j < kBackSums; ++j)
+            t[j] = __shfl_sync(0xffffffffu, all, 4 * j);
+        float gt = 1.0f;
+        if constexpr (GATE == kGateToken)
+            gt = a.gate ? __ldg(static_cast<const float *>(a.gate) + row) : 1.0f;
+        const float r2 = 1.0f / sqrtf(fmaf(t[0], invK, a.eps_pre));
+        const float c2 = r2 * r2 * r2 * (t[1] * invK);
+        const float r1 = POST ? 1.0f / sqrtf(fmaf(t[2], invK, a.eps_post)) : 1.0f;
+        const float sp = fmaf(-c2, t[5], fmaf(r2, t[4], t[3])); // sum p D
         const float c1 = r1 * r1 * r1 * (gt * sp * invK);
         if constexpr (GATE == kGateToken)
             if (a.dgate_tok && threadIdx.x == 0 && rank == 0)
                 a.dgate_tok[row] = r1 * sp;
         if (on) {
-            float o[8], t8[8];
+            uint32_t ores[4], ody[4], ogate[4];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float w = dz[i] * gpre[i];
-                D[i] = fmaf(r2, w, D[i]) - c2 * h[i];
-                acc_pre[i] = fmaf(dz[i] * r2, h[i], acc_pre[i]);
-                t8[i] = D[i] * a.res_scale;
+            for (int hv = 0; hv < 2; ++hv) {
+                const uint2 dz = st[hv], y = st[next + hv], h = st[2 * next + hv];
+                const uint2 dh = has_dh ? st[3 * next + hv] : make_uint2(0u, 0u);
+                uint2 g = make_uint2(0u, 0u);
+                if constexpr (GATE == kGateFull)
+                    g = st[(arrays - 1) * next + hv];
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const float2 dz2 = bf16_pair(dz, e), y2 = bf16_pair(y, e), h2 = bf16_pair(h, e);
+                    const float2 dh2 = bf16_pair(dh, e), g2 = bf16_pair(g, e);
+                    float od[2], oy[2], og[2];
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        const int i = 4 * hv + 2 * e + c;
+                        const float hh = c ? h2.y : h2.x, x1 = (c ? y2.y : y2.x) * r1;
+                        const float zz = c ? dz2.y : dz2.x;
+                        const float D = fmaf(r2, zz * gp[i], fmaf(-c2, hh, c ? dh2.y : dh2.x));
+                        acc_pre[i] = fmaf(zz * r2, hh, acc_pre[i]);
+                        od[c] = D * a.res_scale;
+                        // a gate that varies along the row is in gq (per channel) or in g
+                        const float gd = GATE == kGateToken ? gt * D
+                                         : GATE == kGateFull ? (c ? g2.y : g2.x) * D : D;
+                        if constexpr (kT)
+                            acc_t[i] = fmaf(gd, x1, acc_t[i]);
+                        if constexpr (GATE == kGateFull)
+                            og[c] = D * (x1 * gq[i]);
+                        oy[c] = POST ? fmaf(r1 * gq[i], gd, -c1 * (c ? y2.y : y2.x)) : gq[i] * gd;
+                    }
+                    ores[2 * hv + e] = pack_bf16x2(od[0], od[1]);
+                    ody[2 * hv + e] = pack_bf16x2(oy[0], oy[1]);
+                    if constexpr (GATE == kGateFull)
+                        ogate[2 * hv + e] = pack_bf16x2(og[0], og[1]);
+                }
             }
             const int64_t off = row * nvec + vi;
-            reinterpret_cast<uint4 *>(a.dres)[off] =
-                make_uint4(pack_bf16x2(t8[0], t8[1]), pack_bf16x2(t8[2], t8[3]),
-                           pack_bf16x2(t8[4], t8[5]), pack_bf16x2(t8[6], t8[7]));
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float x1 = y[i] * r1;
-                const float gate = GATE == kGateToken ? gt : g[i];
-                if constexpr (GATE == kGateChannel)
-                    acc_t[i] = fmaf(D[i], x1, acc_t[i]);
-                else
-                    acc_t[i] = fmaf(gate * D[i], x1, acc_t[i]);
-                if constexpr (GATE == kGateFull)
-                    t8[i] = D[i] * (x1 * gpost[i]);
-                if constexpr (POST)
-                    o[i] = fmaf(r1 * gpost[i], gate * D[i], -c1 * y[i]);
-                else
-                    o[i] = gate * D[i];
-            }
-            reinterpret_cast<uint4 *>(a.dy)[off] =
-                make_uint4(pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3]),
-                           pack_bf16x2(o[4], o[5]), pack_bf16x2(o[6], o[7]));
+            reinterpret_cast<uint4 *>(a.dres)[off] = make_uint4(ores[0], ores[1], ores[2], ores[3]);
+            reinterpret_cast<uint4 *>(a.dy)[off] = make_uint4(ody[0], ody[1], ody[2], ody[3]);
             if constexpr (GATE == kGateFull)
                 reinterpret_cast<uint4 *>(a.dgate_full)[off] =
-                    make_uint4(pack_bf16x2(t8[0], t8[1]), pack_bf16x2(t8[2], t8[3]),
-                               pack_bf16x2(t8[4], t8[5]), pack_bf16x2(t8[6], t8[7]));
+                    make_uint4(ogate[0], ogate[1], ogate[2], ogate[3]);
+        }
+        if (++s == a.stages) {
+            s = 0;
+            ph ^= 1u;
         }
     }
     if (on) {
         float4 *p0 = reinterpret_cast<float4 *>(a.part + (static_cast<int64_t>(cl) * 2) * K) + 2 * vi;
         p0[0] = make_float4(acc_pre[0], acc_pre[1], acc_pre[2], acc_pre[3]);
         p0[1] = make_float4(acc_pre[4], acc_pre[5], acc_pre[6], acc_pre[7]);
-        if constexpr (POST || GATE == kGateChannel) {
+        if constexpr (kT) {
             float4 *p1 = p0 + K / 4;
             p1[0] = make_float4(acc_t[0], acc_t[1], acc_t[2], acc_t[3]);
             p1[1] = make_float4(acc_t[4], acc_t[5], acc_t[6], acc_t[7]);
