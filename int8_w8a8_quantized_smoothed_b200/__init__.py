@@ -177,6 +177,14 @@ def _arg(t, name, dtype, shape, index):
     return t.data_ptr()
 
 
+def _out(t, name, dtype, shape, index):
+    """(tensor, address) of an output: the caller's, checked, or a new one."""
+    if t is None:
+        t = torch.empty(shape, dtype=dtype, device=index)
+        return t, t.data_ptr()
+    return t, _arg(t, name, dtype, shape, index)
+
+
 def _matrix(t, name, dtype):
     """(rows, columns, device index) of the tensor that a call takes its sizes from."""
     _need(t, name, dtype)
@@ -788,16 +796,16 @@ def _sandwich_quant(name, code, y, residual, gamma_smoothed, eps, gamma_post, ep
     if residual is None or gamma_smoothed is None:
         raise TypeError("residual and gamma_smoothed must be torch.Tensors")
     kind, pgate = _gate_arg(gate, M, K, index)
-    h_out = torch.empty_like(y) if h_out is None else h_out
-    q = torch.empty((M, K), dtype=code, device=index) if q is None else q
-    s_tok = torch.empty(M, dtype=torch.float32, device=index) if s_tok is None else s_tok
+    shape = (M, K)
+    h_out, ph = _out(h_out, "h_out", torch.bfloat16, shape, index)
+    q, pq = _out(q, "q", code, shape, index)
+    s_tok, ps = _out(s_tok, "s_tok", torch.float32, (M,), index)
     rc = getattr(lib(), name)(
-        y.data_ptr(), _arg(residual, "residual", torch.bfloat16, (M, K), index),
+        y.data_ptr(), _arg(residual, "residual", torch.bfloat16, shape, index),
         _arg(gamma_post, "gamma_post", torch.float32, (K,), index),
         eps if eps_post is None else eps_post, pgate, kind, res_scale,
-        _arg(gamma_smoothed, "gamma_smoothed", torch.float32, (K,), index), eps, M, K,
-        _arg(h_out, "h_out", torch.bfloat16, (M, K), index), _arg(q, "q", code, (M, K), index),
-        _arg(s_tok, "s_tok", torch.float32, (M,), index), _current_stream(index))
+        _arg(gamma_smoothed, "gamma_smoothed", torch.float32, (K,), index), eps, M, K, ph, pq,
+        ps, _current_stream(index))
     if rc:
         raise W8A8Error(name, rc)
     return q, s_tok, h_out
@@ -843,21 +851,20 @@ def w8a8_sandwich_rmsnorm_backward(dz, y, h, gamma_smoothed, eps, dh=None, gamma
         raise TypeError("y, h and gamma_smoothed must be torch.Tensors")
     kind, pgate = _gate_arg(gate, M, K, index)
     L = lib()
-    dy = torch.empty_like(dz) if dy is None else dy
-    dresidual = torch.empty_like(dz) if dresidual is None else dresidual
+    shape = (M, K)
+    dy, pdy = _out(dy, "dy", torch.bfloat16, shape, index)
+    dresidual, pdr = _out(dresidual, "dresidual", torch.bfloat16, shape, index)
     dpre = torch.empty(K, dtype=torch.float32, device=index)
     dpost = None if gamma_post is None else torch.empty(K, dtype=torch.float32, device=index)
     dgate = None if gate is None else torch.empty_like(gate)
     wptr, wbytes, keep = _scratch(
         workspace, L.w8a8_sandwich_rmsnorm_backward_workspace_size(M, K), index)
     rc = L.w8a8_sandwich_rmsnorm_backward(
-        dz.data_ptr(), _arg(dh, "dh", torch.bfloat16, (M, K), index),
-        _arg(y, "y", torch.bfloat16, (M, K), index), _arg(h, "h", torch.bfloat16, (M, K), index),
+        dz.data_ptr(), _arg(dh, "dh", torch.bfloat16, shape, index),
+        _arg(y, "y", torch.bfloat16, shape, index), _arg(h, "h", torch.bfloat16, shape, index),
         _arg(gamma_post, "gamma_post", torch.float32, (K,), index),
         eps if eps_post is None else eps_post, pgate, kind, res_scale,
-        _arg(gamma_smoothed, "gamma_smoothed", torch.float32, (K,), index), eps, M, K,
-        _arg(dy, "dy", torch.bfloat16, (M, K), index),
-        _arg(dresidual, "dresidual", torch.bfloat16, (M, K), index),
+        _arg(gamma_smoothed, "gamma_smoothed", torch.float32, (K,), index), eps, M, K, pdy, pdr,
         None if dpost is None else dpost.data_ptr(), None if dgate is None else dgate.data_ptr(),
         dpre.data_ptr(), wptr, wbytes, _current_stream(index))
     if rc:
@@ -892,11 +899,10 @@ def _grad(name, code, dy, q, scale, rows, out, out_name, gate_up, workspace):
         shape = (M, 2 * K)
         extra = (_arg(gate_up, "gate_up", torch.bfloat16, shape, index),)
     L = lib()
-    out = torch.empty(shape, dtype=torch.bfloat16, device=index) if out is None else out
+    out, pout = _out(out, out_name, torch.bfloat16, shape, index)
     size = L.w8a8_gemm_dgrad_workspace_size if rows else L.w8a8_gemm_wgrad_workspace_size
     wptr, wbytes, keep = _scratch(workspace, size(M, N, K), index)
-    rc = getattr(L, name)(dy.data_ptr(), pq, ps, M, N, K, *extra,
-                          _arg(out, out_name, torch.bfloat16, shape, index), wptr, wbytes,
+    rc = getattr(L, name)(dy.data_ptr(), pq, ps, M, N, K, *extra, pout, wptr, wbytes,
                           _current_stream(index))
     if rc:
         raise W8A8Error(name, rc)

@@ -60,6 +60,57 @@ int launch_sandwich(const SandwichArgs &a, int threads, int dev, int sms, cudaSt
                          a.eps_pre, a.K, static_cast<int>(a.M), a.h, a.q, a.s);
 }
 
+// From this many values on, a call with rows of up to kRowsMaxK of them runs sandwich_rows_kernel
+// (us, this kernel / one row a CTA: 300 x 4096 7.2 / 5.0, 600 x 4096 8.1 / 8.7, 333 x 5136 8.2 / 9.4,
+// 8192 x 4096 with an elementwise gate 59 / 90; it begins by copying the gains).
+constexpr int64_t kRowsFrom = 3 << 19;
+
+template <int W, bool POST, int GATE, bool F8>
+int launch_sandwich_rows_w(const SandwichArgs &a, int dev, int sms, cudaStream_t st)
+{
+    constexpr int kArrays = GATE == kGateFull ? 3 : 2;
+    constexpr int kGains = 1 + (POST ? 1 : 0) + (GATE == kGateChannel ? 1 : 0);
+    constexpr int kMax = 226 * 1024;
+    const int64_t grid = std::min<int64_t>(a.M, sms);
+    int teams = static_cast<int>(std::min<int64_t>(512 / (32 * W), (a.M + grid - 1) / grid));
+    while (teams > 1 && rows_smem_bytes(a.K, kArrays, kGains, teams) > kMax)
+        --teams;
+    auto kernel = sandwich_rows_kernel<W, POST, GATE, F8>;
+    static_assert(rows_smem_bytes(kRowsMaxK, 3, 3, 1) <= kMax, "shared memory per CTA");
+    if (int rc = ensure_smem(reinterpret_cast<const void *>(kernel), dev, kMax))
+        return rc;
+    const SandwichRows r{a.y, a.res, a.gamma_post, a.gamma_pre, a.gate, a.h, a.q, a.s,
+                         a.res_scale, a.eps_post, a.eps_pre, a.K, static_cast<int>(a.M), teams,
+                         kWaitLimitNs};
+    return launch_kernel(kernel, dim3(static_cast<unsigned>(grid)), dim3(teams * 32 * W),
+                         rows_smem_bytes(a.K, kArrays, kGains, teams), st, r);
+}
+
+template <bool POST, int GATE, bool F8>
+int launch_sandwich_rows_t(const SandwichArgs &a, int dev, int sms, cudaStream_t st)
+{
+    constexpr int kPerWarp = kRowsMaxK / 4;
+    return a.K <= kPerWarp       ? launch_sandwich_rows_w<1, POST, GATE, F8>(a, dev, sms, st)
+           : a.K <= 2 * kPerWarp ? launch_sandwich_rows_w<2, POST, GATE, F8>(a, dev, sms, st)
+                                 : launch_sandwich_rows_w<4, POST, GATE, F8>(a, dev, sms, st);
+}
+
+template <bool F8>
+int launch_sandwich_rows(const SandwichArgs &a, int gate_kind, int dev, int sms, cudaStream_t st)
+{
+    switch (gate_kind) {
+    case kGateFull:
+        return a.gamma_post ? launch_sandwich_rows_t<true, kGateFull, F8>(a, dev, sms, st)
+                            : launch_sandwich_rows_t<false, kGateFull, F8>(a, dev, sms, st);
+    case kGateChannel:
+        return a.gamma_post ? launch_sandwich_rows_t<true, kGateChannel, F8>(a, dev, sms, st)
+                            : launch_sandwich_rows_t<false, kGateChannel, F8>(a, dev, sms, st);
+    default:
+        return a.gamma_post ? launch_sandwich_rows_t<true, kGateToken, F8>(a, dev, sms, st)
+                            : launch_sandwich_rows_t<false, kGateToken, F8>(a, dev, sms, st);
+    }
+}
+
 template <int NCH, bool POST, bool F8>
 int launch_sandwich_gate(const SandwichArgs &a, int gate_kind, int threads, int dev, int sms,
                          cudaStream_t st)
@@ -118,6 +169,8 @@ int sandwich_quant_impl(const uint16_t *y, const uint16_t *residual, const float
                          M, static_cast<int>(K), h_out, q, s_tok};
     const RowLaunch L = row_launch(K);
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    if (K <= kRowsMaxK && M * K >= kRowsFrom)
+        return launch_sandwich_rows<F8>(a, gate_kind, dev, sms, st);
     switch (L.nch) {
     case 1: return launch_sandwich_post<1, F8>(a, gate_kind, L.threads, dev, sms, st);
     case 2: return launch_sandwich_post<2, F8>(a, gate_kind, L.threads, dev, sms, st);

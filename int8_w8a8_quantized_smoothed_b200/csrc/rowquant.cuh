@@ -209,6 +209,35 @@ __device__ __forceinline__ uint2 quant_e4m3_8_exact(const float (&y)[8], float s
     return make_uint2(e[0] | (e[1] << 16), e[2] | (e[3] << 16));
 }
 
+// The eight codes of a vector given the row's scale s, r = RN(1 / s) and by_product (s large enough
+// for the reciprocal): E4M3 or int8, value i in byte i. An all-zero row (amax = 0) gives +0 codes.
+template <bool F8>
+__device__ __forceinline__ uint2 quantize_vector(const float (&v)[8], float amax, float s, float r,
+                                                 bool by_product)
+{
+    uint2 out = make_uint2(0u, 0u);
+    if constexpr (F8) {
+        if (by_product)
+            out = quant_e4m3_8(v, s, __fmul_rn(r, kBracketLo), __fmul_rn(r, kBracketHi));
+        else if (amax > 0.0f)
+            out = quant_e4m3_8_exact(v, s);
+    } else if (by_product) {
+        uint32_t b[8];
+        quant_bits8(v, s, r, b);
+        out.x = pack_low_bytes(b[0], b[1], b[2], b[3]);
+        out.y = pack_low_bytes(b[4], b[5], b[6], b[7]);
+    } else if (amax > 0.0f) {
+        out.x = pack_low_bytes(quant_bits(v[0], s), quant_bits(v[1], s), quant_bits(v[2], s),
+                               quant_bits(v[3], s));
+        out.y = pack_low_bytes(quant_bits(v[4], s), quant_bits(v[5], s), quant_bits(v[6], s),
+                               quant_bits(v[7], s));
+    }
+    return out;
+}
+
+// the product path needs a finite reciprocal; scales below 2^-100 take the exact quotient
+constexpr float kProductScale = 7.888609052210118e-31f;
+
 // Quantizes the part of a row held in registers (v[c][0..7] for vector v0 + c*blockDim + tid,
 // vectors below v1) given the row's absmax, writes its codes; the CTA's thread 0 writes the
 // scale when s_out is given. F8: E4M3 codes with s = amax / 448, else int8 with s = amax / 127.
@@ -220,32 +249,13 @@ __device__ __forceinline__ void quantize_and_store(const float (&v)[NCH][8], flo
     const float s = __fdiv_rn(amax, F8 ? 448.0f : 127.0f);
     if (s_out && threadIdx.x == 0)
         *s_out = s;
-    // the product path needs a finite reciprocal; tiny scales take the exact quotient
-    const bool by_product = s >= 7.888609052210118e-31f; // 2^-100
+    const bool by_product = s >= kProductScale;
     const float r = by_product ? __frcp_rn(s) : 0.0f;
 #pragma unroll
     for (int c = 0; c < NCH; ++c) {
         const int vi = v0 + c * blockDim.x + threadIdx.x;
-        if (vi < v1) {
-            uint2 out = make_uint2(0u, 0u); // an all-zero row: s = 0, every code +0
-            if constexpr (F8) {
-                if (by_product)
-                    out = quant_e4m3_8(v[c], s, __fmul_rn(r, kBracketLo), __fmul_rn(r, kBracketHi));
-                else if (amax > 0.0f)
-                    out = quant_e4m3_8_exact(v[c], s);
-            } else if (by_product) {
-                uint32_t b[8];
-                quant_bits8(v[c], s, r, b);
-                out.x = pack_low_bytes(b[0], b[1], b[2], b[3]);
-                out.y = pack_low_bytes(b[4], b[5], b[6], b[7]);
-            } else if (amax > 0.0f) {
-                out.x = pack_low_bytes(quant_bits(v[c][0], s), quant_bits(v[c][1], s),
-                                       quant_bits(v[c][2], s), quant_bits(v[c][3], s));
-                out.y = pack_low_bytes(quant_bits(v[c][4], s), quant_bits(v[c][5], s),
-                                       quant_bits(v[c][6], s), quant_bits(v[c][7], s));
-            }
-            reinterpret_cast<uint2 *>(qrow)[vi] = out;
-        }
+        if (vi < v1)
+            reinterpret_cast<uint2 *>(qrow)[vi] = quantize_vector<F8>(v[c], amax, s, r, by_product);
     }
 }
 

@@ -135,6 +135,241 @@ __global__ void __launch_bounds__(NCH <= 2 ? 256 : 1024, NCH <= 2 ? 3 : 1)
     }
 }
 
+// Many rows of up to 8192 values. What bounded the kernel above was the chain of steps of one row
+// (three reductions over a whole CTA, each with a barrier, and between them square roots and
+// quotients): three CTAs an SM, each at one row, took 90 us for 8192 x 4096 with an elementwise
+// gate, whether their loads were ahead or not. Here a row belongs to a team of one, two or four
+// warps, 64 values a lane, so that up to sixteen rows of an SM are at different steps and a row's
+// reductions cost few instructions. A team's row comes by bulk copies into its place in shared
+// memory, given back as soon as h is formed; the gains are kept in shared memory for all teams.
+struct SandwichRows {
+    const uint16_t *y, *res;
+    const float *gamma_post, *gamma_pre;
+    const void *gate;
+    uint16_t *h;
+    int8_t *q;
+    float *s_tok;
+    float res_scale, eps_post, eps_pre;
+    int K, M, teams;
+    unsigned long long limit_ns;
+};
+
+constexpr int kTeamVecs = 8; // vectors of 8 values a lane
+constexpr int kRowsMaxK = 4 * 32 * kTeamVecs * 8;
+
+// Shared memory: the gains as two planes of half vectors each (so that lanes' reads of 16 bytes
+// are consecutive), each team's row, its barrier and its sums.
+__host__ __device__ constexpr int rows_smem_bytes(int K, int arrays, int gains, int teams)
+{
+    return K * 4 * gains + teams * (2 * K * arrays + 8 + 2 * 4 * 8 + 4 * 4);
+}
+
+template <int W> __device__ __forceinline__ void team_sync(int team)
+{
+    if constexpr (W == 1)
+        __syncwarp();
+    else
+        named_bar_sync(1 + team, 32 * W);
+}
+
+// Running sum of squares of values that are exact in bf16 (so are their squares in binary32): a
+// binary32 sum and the sum of its additions' exact errors, two lanes at a time. The two carry
+// about 2^-46 of the sum, with a fraction of the time of binary64 conversions and additions.
+struct SquareSum {
+    float2 hi = make_float2(0.0f, 0.0f), lo = make_float2(0.0f, 0.0f);
+    __device__ __forceinline__ void add(float2 a)
+    {
+        const float2 m1 = make_float2(-1.0f, -1.0f);
+        const float2 p = mul2(a, a);
+        const float2 t = add2(hi, p);
+        const float2 z = fma2(hi, m1, t); // t - hi
+        lo = add2(lo, add2(fma2(fma2(z, m1, t), m1, hi), fma2(z, m1, p))); // (hi - (t - z)) + (p - z)
+        hi = t;
+    }
+    __device__ __forceinline__ double value() const
+    {
+        return (static_cast<double>(hi.x) + static_cast<double>(hi.y)) +
+               (static_cast<double>(lo.x) + static_cast<double>(lo.y));
+    }
+};
+
+template <int W>
+__device__ __forceinline__ double team_sum(double v, double *sh, int team, int warp_in_team, int lane)
+{
+    v = warp_sum(v);
+    if constexpr (W > 1) {
+        if (lane == 0)
+            sh[warp_in_team] = v;
+        team_sync<W>(team);
+        v = sh[0];
+#pragma unroll
+        for (int w = 1; w < W; ++w)
+            v = __dadd_rn(v, sh[w]);
+    }
+    return v;
+}
+
+template <int W, bool POST, int GATE, bool F8>
+__global__ void __launch_bounds__(512, 1) sandwich_rows_kernel(const SandwichRows a)
+{
+    extern __shared__ __align__(16) uint8_t rows_smem[];
+    constexpr int kArrays = GATE == kGateFull ? 3 : 2;
+    constexpr int kGains = 1 + (POST ? 1 : 0) + (GATE == kGateChannel ? 1 : 0);
+    const int nvec = a.K >> 3;
+    const int lane = threadIdx.x & 31;
+    const int team = threadIdx.x / (32 * W), tl = threadIdx.x % (32 * W), wt = tl >> 5;
+    float4 *gains = reinterpret_cast<float4 *>(rows_smem); // [gain][half][nvec]
+    uint4 *rows = reinterpret_cast<uint4 *>(gains + kGains * 2 * nvec);
+    uint64_t *bars = reinterpret_cast<uint64_t *>(rows + a.teams * kArrays * nvec);
+    double *sums = reinterpret_cast<double *>(bars + a.teams) + team * 8; // two of four
+    float *maxes = reinterpret_cast<float *>(reinterpret_cast<double *>(bars + a.teams) + a.teams * 8) +
+                   team * 4;
+    const uint32_t bar = smem_u32(bars + team);
+    if (tl == 0) {
+        mbar_init(bar, 1);
+        fence_mbar_init();
+    }
+    if (threadIdx.x == 0)
+        pdl_launch_dependents();
+    __syncthreads();
+    pdl_wait(); // every input may come from the previous kernel
+    const int64_t stride = static_cast<int64_t>(gridDim.x) * a.teams;
+    const int64_t first = blockIdx.x + static_cast<int64_t>(team) * gridDim.x;
+    const uint4 *mine = rows + team * kArrays * nvec;
+    auto fetch = [&](int64_t row) { // one thread of the team
+        const uint32_t bytes = static_cast<uint32_t>(nvec) * 16, dst = smem_u32(mine);
+        const int64_t at = row * nvec;
+        mbar_expect_tx(bar, bytes * kArrays);
+        bulk_load_g2s(dst, reinterpret_cast<const uint4 *>(a.y) + at, bytes, bar);
+        bulk_load_g2s(dst + bytes, reinterpret_cast<const uint4 *>(a.res) + at, bytes, bar);
+        if constexpr (GATE == kGateFull)
+            bulk_load_g2s(dst + 2 * bytes, static_cast<const uint4 *>(a.gate) + at, bytes, bar);
+    };
+    if (tl == 0 && first < a.M)
+        fetch(first);
+    auto keep = [&](const float *src, int gain) {
+        for (int i = threadIdx.x; i < 2 * nvec; i += blockDim.x)
+            gains[(gain * 2 + (i & 1)) * nvec + (i >> 1)] =
+                __ldg(reinterpret_cast<const float4 *>(src) + i);
+    };
+    keep(a.gamma_pre, 0);
+    if constexpr (POST)
+        keep(a.gamma_post, 1);
+    if constexpr (GATE == kGateChannel)
+        keep(static_cast<const float *>(a.gate), kGains - 1);
+    __syncthreads();
+    auto gain8 = [&](int gain, int vi, float (&g)[8]) {
+        const float4 x = gains[gain * 2 * nvec + vi], y = gains[(gain * 2 + 1) * nvec + vi];
+        g[0] = x.x; g[1] = x.y; g[2] = x.z; g[3] = x.w;
+        g[4] = y.x; g[5] = y.y; g[6] = y.z; g[7] = y.w;
+    };
+    uint32_t ph = 0;
+    for (int64_t row = first; row < a.M; row += stride, ph ^= 1u) {
+        // a wait that ran out has raised the status word; the row is then worked on as it is
+        (void)mbar_wait(bar, ph, a.limit_ns);
+        __syncwarp();
+        float v[kTeamVecs][8];
+        float r1 = 1.0f;
+        if constexpr (POST) {
+            SquareSum ss;
+#pragma unroll
+            for (int c = 0; c < kTeamVecs; ++c) {
+                const int vi = c * 32 * W + tl;
+                if (vi < nvec) {
+                    unpack8(mine[vi], v[c]);
+#pragma unroll
+                    for (int i = 0; i < 8; i += 2)
+                        ss.add(make_float2(v[c][i], v[c][i + 1]));
+                }
+            }
+            r1 = rstd_of(team_sum<W>(ss.value(), sums, team, wt, lane), a.K, a.eps_post);
+        }
+        float gt = 1.0f;
+        if constexpr (GATE == kGateToken)
+            gt = a.gate ? __ldg(static_cast<const float *>(a.gate) + row) : 1.0f;
+        SquareSum ss;
+#pragma unroll
+        for (int c = 0; c < kTeamVecs; ++c) {
+            const int vi = c * 32 * W + tl;
+            if (vi < nvec) {
+                float r[8], g[8];
+                unpack8(mine[vi], v[c]);
+                uint32_t w[4];
+                if constexpr (POST) {
+                    gain8(1, vi, g);
+#pragma unroll
+                    for (int i = 0; i < 8; i += 2) {
+                        const float2 x = mul2(mul2(make_float2(v[c][i], v[c][i + 1]), splat2(r1)),
+                                              make_float2(g[i], g[i + 1]));
+                        v[c][i] = x.x;
+                        v[c][i + 1] = x.y;
+                    }
+                }
+                if constexpr (GATE == kGateFull)
+                    unpack8(mine[2 * nvec + vi], g);
+                else if constexpr (GATE == kGateChannel)
+                    gain8(kGains - 1, vi, g);
+                unpack8(mine[nvec + vi], r);
+#pragma unroll
+                for (int i = 0; i < 8; i += 2) {
+                    float2 x = mul2(GATE == kGateToken ? splat2(gt) : make_float2(g[i], g[i + 1]),
+                                    make_float2(v[c][i], v[c][i + 1]));
+                    x = add2(mul2(splat2(a.res_scale), make_float2(r[i], r[i + 1])), x);
+                    w[i >> 1] = pack_bf16x2(x.x, x.y);
+                }
+                const uint4 hb = make_uint4(w[0], w[1], w[2], w[3]);
+                reinterpret_cast<uint4 *>(a.h)[row * nvec + vi] = hb;
+                unpack8(hb, v[c]);
+#pragma unroll
+                for (int i = 0; i < 8; i += 2)
+                    ss.add(make_float2(v[c][i], v[c][i + 1]));
+            }
+        }
+        const float r2 = rstd_of(team_sum<W>(ss.value(), sums + 4, team, wt, lane), a.K, a.eps_pre);
+        // the whole team has used what it read of this row: its place is free
+        if (tl == 0 && row + stride < a.M)
+            fetch(row + stride);
+        float amax = 0.0f;
+#pragma unroll
+        for (int c = 0; c < kTeamVecs; ++c) {
+            const int vi = c * 32 * W + tl;
+            if (vi < nvec) {
+                float g[8];
+                gain8(0, vi, g);
+#pragma unroll
+                for (int i = 0; i < 8; i += 2) {
+                    const float2 x = mul2(mul2(make_float2(v[c][i], v[c][i + 1]), splat2(r2)),
+                                          make_float2(g[i], g[i + 1]));
+                    v[c][i] = x.x;
+                    v[c][i + 1] = x.y;
+                    amax = fmaxf(amax, fmaxf(fabsf(x.x), fabsf(x.y)));
+                }
+            }
+        }
+        amax = warp_max(amax);
+        if constexpr (W > 1) {
+            if (lane == 0)
+                maxes[wt] = amax;
+            team_sync<W>(team);
+#pragma unroll
+            for (int w = 0; w < W; ++w)
+                amax = fmaxf(amax, maxes[w]);
+        }
+        const float s = __fdiv_rn(amax, F8 ? 448.0f : 127.0f);
+        if (tl == 0)
+            a.s_tok[row] = s;
+        const bool by_product = s >= kProductScale;
+        const float rs = by_product ? __frcp_rn(s) : 0.0f;
+#pragma unroll
+        for (int c = 0; c < kTeamVecs; ++c) {
+            const int vi = c * 32 * W + tl;
+            if (vi < nvec)
+                reinterpret_cast<uint2 *>(a.q)[row * nvec + vi] =
+                    quantize_vector<F8>(v[c], amax, s, rs, by_product);
+        }
+    }
+}
+
 // ------------------------------------------------------------------------------ backward
 //
 // With w = dz gamma_pre and p = gamma_post y (p = y without the first norm), per row:

@@ -1,8 +1,6 @@
 """Parity of the block-boundary norms: h bit for bit against the formula's binary32 operations,
 codes and scales against the oracle's RMSNorm + quantization of that h, and the backward pass
 against the binary64 formula within the bound that its magnitudes give."""
-import math
-
 import numpy as np
 import pytest
 import torch
@@ -19,6 +17,8 @@ pytestmark = pytest.mark.gpu
 EPS, EPS_POST = 1e-5, 1e-3
 SHAPES = [(1, 16), (1, 4096), (3, 48), (37, 4096), (5, 8192), (7, 4112), (33, 1040), (2, 14336),
           (2, 32768), (700, 272)]
+# enough values for the kernel in which one, two or four warps share a row
+MANY = [(1600, 1040), (400, 4096), (400, 4112)]
 GATES = ["none", "token", "channel", "full"]
 
 
@@ -36,8 +36,8 @@ def _gate(kind, M, K, seed):
 
 
 def _rstd32(x, eps):
-    """1 / sqrt(ms + eps) in binary32, ms the exactly summed mean of squares rounded once."""
-    ms = np.array([math.fsum(r) / x.shape[1] for r in x.astype(np.float64) ** 2])
+    """1 / sqrt(ms + eps) in binary32, ms the mean of squares summed with 64 bits and rounded."""
+    ms = (x.astype(np.float64) ** 2).astype(np.longdouble).sum(axis=1) / x.shape[1]
     return np.float32(1.0) / np.sqrt(ms.astype(np.float32) + np.float32(eps))
 
 
@@ -62,7 +62,7 @@ def _f(b):
     return oracle.bf16_to_f32(b).reshape(b.shape)
 
 
-@pytest.mark.parametrize("M,K", SHAPES)
+@pytest.mark.parametrize("M,K", SHAPES + MANY)
 @pytest.mark.parametrize("kind", GATES)
 @pytest.mark.parametrize("post", [False, True])
 @pytest.mark.parametrize("f8", [False, True])
@@ -90,8 +90,8 @@ def test_forward_matches_oracle(M, K, kind, post, f8):
                           oracle.smooth_rmsnorm_quant)
 
 
-def test_forward_in_place_and_zero_rows():
-    M, K = 6, 512
+@pytest.mark.parametrize("M,K", [(6, 512), (900, 2048)])
+def test_forward_in_place_and_zero_rows(M, K):
     y, res, gs, gp = _inputs(M, K, True, 3)
     y[2] = 0
     res[2] = 0   # nothing in the row: h = 0, s = 0, every code 0
@@ -115,9 +115,9 @@ def test_forward_zero_row_with_eps():
     assert not host(q).any() and not host(s).any() and not h.any()
 
 
-def test_forward_without_extras_equals_the_residual_norm():
+@pytest.mark.parametrize("M,K", [(40, 4096), (500, 4096)])
+def test_forward_without_extras_equals_the_residual_norm(M, K):
     """No post norm, no gate, scale 1: the residual form of w8a8_smooth_rmsnorm_quant."""
-    M, K = 40, 4096
     y, res, gs, _ = _inputs(M, K, False, 11)
     q0, s0, h0 = w8.w8a8_smooth_rmsnorm_quant(dev_bf16(y), dev(gs), EPS, residual=dev_bf16(res))
     q1, s1, h1 = w8.w8a8_sandwich_rmsnorm_quant(dev_bf16(y), dev_bf16(res), dev(gs), EPS)
@@ -135,7 +135,7 @@ def _check(name, got, ref, mag, roundings, stored_bf16):
     assert not bad.any(), (name, int(bad.sum()), float((err / np.maximum(tol, 1e-300)).max()))
 
 
-@pytest.mark.parametrize("M,K", SHAPES)
+@pytest.mark.parametrize("M,K", SHAPES + [(700, 4096), (150, 8192)])
 @pytest.mark.parametrize("kind", GATES)
 @pytest.mark.parametrize("post", [False, True])
 @pytest.mark.parametrize("with_dh", [False, True])
