@@ -100,13 +100,12 @@ struct GradBlocks {
 
 // CONV: the kernel converts Q itself; otherwise B is a bf16 matrix loaded like A.
 template <bool CONV> struct GradCfg {
-    static constexpr int STAGES = CONV ? 5 : 6;
-    static constexpr int QSTAGES = CONV ? 4 : 0;
-    // A converter group meets a stage of Q again only after it has used it before (see the narrow
-    // kernel's). Of the other ring it may meet one that another group used: it comes there having
-    // finished the k-block kGradConvGroups before, so the MMAs of STAGES k-blocks before that one,
-    // and of all earlier ones, are done, and it cannot be two rounds early.
-    static_assert(QSTAGES % kGradConvGroups == 0 && STAGES >= kGradConvGroups, "rings and groups");
+    static constexpr int STAGES = CONV ? 4 : 6;
+    static constexpr int QSTAGES = CONV ? 8 : 0; // two a group: one is loaded meanwhile
+    // A converter group meets a stage of either ring again only after it has used it before (see
+    // the narrow kernel's).
+    static_assert(QSTAGES % kGradConvGroups == 0 && (!CONV || STAGES % kGradConvGroups == 0),
+                  "rings and groups");
     static constexpr int kThreads = CONV ? kGradThreads : 256; // without: no converter warps
     static constexpr int kABytes = 128 * kGradBR * 2;
     static constexpr int kBBytes = 128 * kGradBR * 2;
