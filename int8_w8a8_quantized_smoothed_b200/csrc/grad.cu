@@ -273,10 +273,11 @@ struct GradPlan {
 
 // Up to this many rows i an input gradient runs the narrow kernel.
 constexpr int64_t kGradNarrowRows = 128;
-// From this many rows i on, Q is converted once ahead of the product. The kernel that converts
-// its tiles itself does each of them again for every 256 rows and runs at about 1.1 PFLOP/s, the
-// other at about 1.4, after a pass over Q of 3 bytes a code.
-constexpr int64_t kGradDequantRows = 1024;
+// From this many rows i on, Q is converted once ahead of the product: a pass over Q of 3 bytes a
+// code, after which the GEMM is free of the conversions that the other form makes again for every
+// 256 rows (us, that form / this: 512 x 14336 x 4096 68 / 94, 2048 x 28672 x 4096 390 / 425,
+// 4096 x 8192 x 4096 225 / 212, 8192 x 4096 x 4096 213 / 185).
+constexpr int64_t kGradDequantRows = 4096;
 
 // False when there are more tiles than an int counts.
 bool grad_plan(int64_t I, int64_t J, int64_t R, bool wgrad, int sms, GradPlan *p)

@@ -160,6 +160,15 @@ __device__ __forceinline__ uint64_t sw128_mnmajor_desc(uint32_t saddr)
     return d;
 }
 
+// Arrive on an mbarrier of either CTA of the pair (a cluster address). Release at CTA scope: what
+// it publishes are stores to this CTA's own shared memory, behind a proxy fence of every thread
+// that made them, for the pair's MMA. At cluster scope the arrival itself took about 2000 cycles,
+// which four groups of converters could not hide (2048 x 28672 x 4096 440 us, now 390).
+__device__ __forceinline__ void mbar_arrive_pair(uint32_t bar_cluster)
+{
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar_cluster) : "memory");
+}
+
 // A ring's stage and the parity of its current round, kept running: the single-thread roles are
 // chains of dependent instructions, and a remainder by the number of stages in each of them
 // (with addresses computed anew) made a k-block's issue take 650 cycles.
@@ -676,7 +685,7 @@ __global__ void __launch_bounds__(GradCfg<CONV>::kThreads, 1)
             fence_proxy_async_smem(); // the tensor cores read what was stored
             __syncwarp();
             if (lane == 0) {
-                mbar_arrive_cluster(full0 + 8 * s);
+                mbar_arrive_pair(full0 + 8 * s);
                 // Q's stage goes back only here: an arrival does not wait for loads in flight, and
                 // right after the loads (stores of other warps before them in the queue) the next
                 // bulk copy overwrote bytes not yet read, in one call of two hundred

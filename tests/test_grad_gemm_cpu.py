@@ -54,11 +54,11 @@ def test_workspace_sizes(L):
     assert d(4, 12, 64) == 0 and d(0, 64, 64) == 0  # refused shapes
     assert d(1, 4096, 4096) == 148 * narrow         # 32 tiles of 64 k-blocks on 148 SMs
     assert d(129, 4096, 256) == 16 * tile           # 64 k-blocks, four for each pair
-    assert d(2048, 72, 4096) == 72 * 4096 * 2       # many rows: the bf16 weight
+    assert d(4096, 72, 4096) == 72 * 4096 * 2       # many rows: the bf16 weight
     assert wg(72, 4096, 4096) == 72 * 4096 * 2      # or the bf16 activations; short sums whole
     assert wg(4096, 256, 256) == 16 * tile
     # the bf16 operand (to 256 bytes), then the partial tiles of a split
-    assert d(1100, 8200, 272) == 8200 * 272 * 2 + 74 * tile
+    assert d(4100, 8200, 272) == 8200 * 272 * 2 + 74 * tile
 
 
 def test_binding_refuses_cpu_tensors():
