@@ -226,6 +226,12 @@ def _scratch(workspace, nbytes, index):
     return ptr, workspace.numel() * workspace.element_size(), workspace
 
 
+@functools.lru_cache(maxsize=4096)
+def _size(name, index, *dims):
+    """A workspace size of the library: a function of the sizes and of device `index` (current)."""
+    return int(getattr(lib(), name)(*dims))
+
+
 def _current_stream(index):
     return torch._C._cuda_getCurrentRawStream(index)
 
@@ -858,7 +864,7 @@ def w8a8_sandwich_rmsnorm_backward(dz, y, h, gamma_smoothed, eps, dh=None, gamma
     dpost = None if gamma_post is None else torch.empty(K, dtype=torch.float32, device=index)
     dgate = None if gate is None else torch.empty_like(gate)
     wptr, wbytes, keep = _scratch(
-        workspace, L.w8a8_sandwich_rmsnorm_backward_workspace_size(M, K), index)
+        workspace, _size("w8a8_sandwich_rmsnorm_backward_workspace_size", index, M, K), index)
     rc = L.w8a8_sandwich_rmsnorm_backward(
         dz.data_ptr(), _arg(dh, "dh", torch.bfloat16, shape, index),
         _arg(y, "y", torch.bfloat16, shape, index), _arg(h, "h", torch.bfloat16, shape, index),
@@ -900,8 +906,8 @@ def _grad(name, code, dy, q, scale, rows, out, out_name, gate_up, workspace):
         extra = (_arg(gate_up, "gate_up", torch.bfloat16, shape, index),)
     L = lib()
     out, pout = _out(out, out_name, torch.bfloat16, shape, index)
-    size = L.w8a8_gemm_dgrad_workspace_size if rows else L.w8a8_gemm_wgrad_workspace_size
-    wptr, wbytes, keep = _scratch(workspace, size(M, N, K), index)
+    size = "w8a8_gemm_dgrad_workspace_size" if rows else "w8a8_gemm_wgrad_workspace_size"
+    wptr, wbytes, keep = _scratch(workspace, _size(size, index, M, N, K), index)
     rc = getattr(L, name)(dy.data_ptr(), pq, ps, M, N, K, *extra, pout, wptr, wbytes,
                           _current_stream(index))
     if rc:

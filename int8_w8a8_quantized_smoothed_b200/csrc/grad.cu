@@ -305,18 +305,25 @@ bool grad_plan(int64_t I, int64_t J, int64_t R, bool wgrad, int sms, GradPlan *p
     w->npairs = static_cast<int>(pairs);
     w->whole = static_cast<int>(tiles / pairs * pairs);
     w->rem = static_cast<int>(tiles % pairs);
+    // The last tiles' k-blocks are split over more pairs (CTAs) where that saves more time than the
+    // partial tiles cost: a k-block takes about 0.4 us (narrow), 0.5 us (converted by the kernel)
+    // or 0.35 us; the second launch about 3 us, and the partial tiles are stored and read at about
+    // 6 MB a us.
     w->rem_pairs = w->rem;
-    if (w->rem > 0) {
-        // The last tiles' k-blocks are split over all pairs (CTAs) where that saves more time
-        // than the partial tiles cost: a k-block takes about 0.4 us (narrow), 0.55 us (converted
-        // by the kernel) or 0.35 us; the second launch about 4 us, storing and adding partial
-        // tiles up to 8 us (by their rows).
+    const double each = narrow ? 0.4 : p->form == kGradConv ? 0.5 : 0.35;
+    const double tile_bytes = 4.0 * std::min<int64_t>(I, w->tile_i) * w->tile_j;
+    double best = each * static_cast<double>(kb);
+    for (int k = 2; w->rem > 0 && k <= 65; ++k) {
         const int64_t split =
-            std::min(pairs, std::max<int64_t>(w->rem, w->rem * kb / (narrow ? 2 : 4)));
-        const double each = narrow ? 0.4 : p->form == kGradConv ? 0.55 : 0.35;
-        const double saved = each * (kb - static_cast<double>(w->rem * kb) / split);
-        if (saved > 4.0 + (narrow ? 0.0 : 8.0 * std::min<int64_t>(I, kGradTile) / kGradTile))
+            std::min(pairs, static_cast<int64_t>(w->rem) * (k <= 64 ? k : pairs));
+        const double share = static_cast<double>((w->rem * kb + split - 1) / split);
+        const double time = each * share + 3.0 + (split + w->rem) * tile_bytes * 2 / 6e6;
+        if (share >= (narrow ? 2 : 4) && time < best) {
+            best = time;
             w->rem_pairs = static_cast<int>(split);
+        }
+        if (split == pairs)
+            break;
     }
     p->part_off = p->form == kGradDequant
                       ? (static_cast<size_t>(R) * static_cast<size_t>(J) * 2 + 255) / 256 * 256
@@ -648,7 +655,7 @@ int w8a8_sandwich_rmsnorm_backward(const w8a8_bf16 *dz, const w8a8_bf16 *dh, con
         return rc;
     return launch_kernel(sandwich_part_kernel,
                          dim3(static_cast<unsigned>((K + 31) / 32), gamma_post || channel ? 2 : 1),
-                         dim3(256), 0, st, static_cast<const float *>(workspace),
+                         dim3(p.clusters > 320 ? 1024 : 256), 0, st, static_cast<const float *>(workspace),
                          static_cast<int>(p.clusters), static_cast<int>(K), gamma_post,
                          channel ? static_cast<const float *>(gate) : nullptr, dgamma_smoothed,
                          dgamma_post, channel ? static_cast<float *>(dgate) : nullptr);

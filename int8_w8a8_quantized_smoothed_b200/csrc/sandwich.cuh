@@ -677,34 +677,41 @@ __global__ void __launch_bounds__(kBackMaxThreads, 1) sandwich_back_kernel(const
         cluster_sync(); // a peer may still read this CTA's sums
 }
 
-// Column sums of the CTAs' parts, in order: dgamma_pre from array 0; T from array 1 gives
-// dgamma_post = [gate_ch] T and dgate_ch = [gamma_post] T. A block takes 32 columns, a warp every
-// eighth part.
-__global__ void __launch_bounds__(256) sandwich_part_kernel(const float *__restrict__ part,
-                                                            int nparts, int K,
-                                                            const float *__restrict__ gamma_post,
-                                                            const float *__restrict__ gate_ch,
-                                                            float *__restrict__ dgamma_pre,
-                                                            float *__restrict__ dgamma_post,
-                                                            float *__restrict__ dgate_ch)
+// Column sums of the CTAs' parts, in a fixed order: dgamma_pre from array 0; T from array 1 gives
+// dgamma_post = [gate_ch] T and dgate_ch = [gamma_post] T. A block takes 32 columns, its warps the
+// parts in turn, four loads of each in flight: 8 warps (which find room beside the kernel before),
+// or 32 for many parts.
+__global__ void __launch_bounds__(1024) sandwich_part_kernel(const float *__restrict__ part,
+                                                             int nparts, int K,
+                                                             const float *__restrict__ gamma_post,
+                                                             const float *__restrict__ gate_ch,
+                                                             float *__restrict__ dgamma_pre,
+                                                             float *__restrict__ dgamma_post,
+                                                             float *__restrict__ dgate_ch)
 {
-    __shared__ float sh[8][32];
+    __shared__ float sh[32][32];
     if (threadIdx.x == 0)
         pdl_launch_dependents();
     pdl_wait();
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, nw = blockDim.x >> 5;
     const int col = blockIdx.x * 32 + lane;
     const int which = blockIdx.y;
+    const float *src = part + static_cast<int64_t>(which) * K + col;
     float t = 0.0f;
     if (col < K)
-        for (int p = warp; p < nparts; p += 8)
-            t += part[(static_cast<int64_t>(p) * 2 + which) * K + col];
+        for (int p = warp; p < nparts; p += 4 * nw) {
+            float v[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                v[e] = p + nw * e < nparts ? __ldcs(src + static_cast<int64_t>(p + nw * e) * 2 * K)
+                                           : 0.0f;
+            t += (v[0] + v[1]) + (v[2] + v[3]);
+        }
     sh[warp][lane] = t;
     __syncthreads();
     if (warp == 0 && col < K) {
         t = 0.0f;
-#pragma unroll
-        for (int w = 0; w < 8; ++w)
+        for (int w = 0; w < nw; ++w)
             t += sh[w][lane];
         if (which == 0) {
             dgamma_pre[col] = t;
