@@ -11,6 +11,7 @@ package does not need a GPU, but every compute call does.
 """
 import ctypes as C
 import functools
+import inspect
 import os
 import threading
 
@@ -197,16 +198,21 @@ def _on_device(fn):
     """Runs a call with its first tensor's device current and on the given stream (default: that
     device's current stream), so that outputs and workspaces allocated inside belong to the stream
     that uses them."""
+    first = next(iter(inspect.signature(fn).parameters))
+
     @functools.wraps(fn)
-    def call(x, *args, stream=None, **kw):
+    def call(*args, stream=None, **kw):
+        x = args[0] if args else kw.get(first)
+        if not isinstance(x, torch.Tensor) or not x.is_cuda:
+            return fn(*args, **kw)  # which says what is wrong with it
         if stream is None:
-            if not x.is_cuda or x.get_device() == torch.cuda.current_device():
-                return fn(x, *args, **kw)
+            if x.get_device() == torch.cuda.current_device():
+                return fn(*args, **kw)
             stream = torch.cuda.current_stream(x.device)
         elif stream.device != x.device:
             raise ValueError(f"stream is on {stream.device}, the tensors on {x.device}")
         with torch.cuda.stream(stream):
-            return fn(x, *args, **kw)
+            return fn(*args, **kw)
     return call
 
 
@@ -809,9 +815,9 @@ def _sandwich_quant(name, code, y, residual, gamma_smoothed, eps, gamma_post, ep
     rc = getattr(lib(), name)(
         y.data_ptr(), _arg(residual, "residual", torch.bfloat16, shape, index),
         _arg(gamma_post, "gamma_post", torch.float32, (K,), index),
-        eps if eps_post is None else eps_post, pgate, kind, res_scale,
-        _arg(gamma_smoothed, "gamma_smoothed", torch.float32, (K,), index), eps, M, K, ph, pq,
-        ps, _current_stream(index))
+        float(eps if eps_post is None else eps_post), pgate, kind, float(res_scale),
+        _arg(gamma_smoothed, "gamma_smoothed", torch.float32, (K,), index), float(eps), M, K, ph,
+        pq, ps, _current_stream(index))
     if rc:
         raise W8A8Error(name, rc)
     return q, s_tok, h_out
@@ -869,8 +875,9 @@ def w8a8_sandwich_rmsnorm_backward(dz, y, h, gamma_smoothed, eps, dh=None, gamma
         dz.data_ptr(), _arg(dh, "dh", torch.bfloat16, shape, index),
         _arg(y, "y", torch.bfloat16, shape, index), _arg(h, "h", torch.bfloat16, shape, index),
         _arg(gamma_post, "gamma_post", torch.float32, (K,), index),
-        eps if eps_post is None else eps_post, pgate, kind, res_scale,
-        _arg(gamma_smoothed, "gamma_smoothed", torch.float32, (K,), index), eps, M, K, pdy, pdr,
+        float(eps if eps_post is None else eps_post), pgate, kind, float(res_scale),
+        _arg(gamma_smoothed, "gamma_smoothed", torch.float32, (K,), index), float(eps), M, K, pdy,
+        pdr,
         None if dpost is None else dpost.data_ptr(), None if dgate is None else dgate.data_ptr(),
         dpre.data_ptr(), wptr, wbytes, _current_stream(index))
     if rc:

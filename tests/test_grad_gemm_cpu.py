@@ -66,3 +66,7 @@ def test_binding_refuses_cpu_tensors():
     q = torch.zeros(64, 128, dtype=torch.int8)
     with pytest.raises(ValueError, match="CUDA"):
         w8.w8a8_gemm_dgrad(dy, q, torch.ones(64))
+    with pytest.raises(ValueError, match="CUDA"):
+        w8.w8a8_gemm_dgrad(dy=dy, wq=q, s_ch=torch.ones(64))
+    with pytest.raises(TypeError, match="dy must be"):
+        w8.w8a8_gemm_wgrad(None, q, torch.ones(64))
