@@ -397,7 +397,8 @@ W8A8_API int w8a8_sandwich_rmsnorm_backward(const w8a8_bf16 *dz, const w8a8_bf16
  * projection itself the rows of wq and the columns of dy only have to agree, so the interleaved
  * weight of w8a8_gemm_silu_quant serves with dy interleaved alike. dx: bf16 [M,K]; dw: bf16 [N,K].
  * Every matrix 16-byte aligned; no output may alias an input. Scales finite and at least
- * 2^-100 or zero; no E4M3 NaN codes.
+ * 2^-100 or zero (one that is not finite makes NaN of all that it reaches, beside zeros too); no
+ * E4M3 NaN codes.
  * Requires M >= 1, N >= 8, N % 8 == 0, K (I) >= 16, K % 16 == 0, each at most 2^30.
  * workspace: w8a8_gemm_dgrad_workspace_size(M, N, K) bytes (dgrad_silu: K = I), or
  * w8a8_gemm_wgrad_workspace_size(M, N, K), 16-byte aligned, any contents (0: may be NULL).

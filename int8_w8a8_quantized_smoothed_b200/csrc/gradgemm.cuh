@@ -8,9 +8,11 @@
 //
 // Both sum over the rows of the 8-bit matrix Q, which is the dimension its scales belong to, so
 // the scale cannot wait for the epilogue: Q becomes a scaled bf16 operand, its codes exact in bf16
-// and the product with the scale rounded once. Two forms:
-//   CONV      warps of the kernel turn Q's tiles into bf16 tiles in shared memory (a code is read
-//             from HBM as one byte and never stored as two), for few rows i;
+// and the product with the scale rounded once. Three forms:
+//   narrow    at most 128 rows i of an input gradient: the codes are streamed once, converted into
+//             tensor memory (below);
+//   CONV      warps of the kernel turn Q's tiles into bf16 tiles in shared memory: a code is read
+//             as one byte and never stored as two;
 //   otherwise grad_dequant_kernel writes all of B first and the kernel loads both operands: each
 //             of Q's tiles is converted once, not once for every tile of rows i.
 // B's tiles keep Q's layout (rows r, j contiguous: the MMA's MN-major form), as does A in the
@@ -21,7 +23,8 @@
 
 namespace w8a8 {
 
-constexpr int kGradThreads = 768; // A producer, MMA, Q producer, idle; 4 epilogue; 16 converters
+// warps: 0 A producer, 1 MMA, 2 Q producer (CONV); 4 .. 7 epilogue; 8 .. 23 converters (CONV)
+constexpr int kGradThreads = 768;
 constexpr int kGradConvWarp0 = 8;
 constexpr int kGradConvWarps = 16;
 constexpr int kGradConvGroups = 4; // groups of converter warps, each on its own k-block
@@ -231,24 +234,25 @@ __device__ __forceinline__ uint32_t fma_bf16x2(uint32_t a, uint32_t b, uint32_t 
     return r;
 }
 
-// A scale as the sum of two bf16 values, the nearest one and the nearest to what it leaves (2^-17
-// relative together), in the upper halves of hi and lo.
-__device__ __forceinline__ void split_scale(float s, uint32_t &hi, uint32_t &lo)
+// Scales as the sum of two bf16 values, the nearest one and the nearest to what it leaves (2^-17
+// relative together); hi and lo hold two scales' each, the first in the lower half. A scale that
+// is not finite leaves a NaN.
+__device__ __forceinline__ void split_scales(float s0, float s1, uint32_t &hi, uint32_t &lo)
 {
-    hi = __float_as_uint(s) + 0x8000u;
-    lo = __float_as_uint(s - __uint_as_float(hi & 0xFFFF0000u)) + 0x8000u;
+    hi = pack_bf16x2(s0, s1);
+    lo = pack_bf16x2(s0 - __uint_as_float(hi << 16), s1 - __uint_as_float(hi & 0xFFFF0000u));
 }
 
-// The same with each part in both halves of a word.
+// One scale's parts in both halves of a word.
 struct RowScale {
     uint32_t hi, lo;
 };
 
 __device__ __forceinline__ RowScale row_scale(float s)
 {
-    uint32_t h, l;
-    split_scale(s, h, l);
-    return RowScale{__byte_perm(h, h, 0x3232), __byte_perm(l, l, 0x3232)};
+    RowScale r;
+    split_scales(s, s, r.hi, r.lo);
+    return r;
 }
 
 // Four codes (a 32-bit word) as exact bf16 values, v[0] the first two.
@@ -1068,13 +1072,9 @@ __global__ void __launch_bounds__(kNarrowThreads, 1)
         fetch();
         for (uint32_t it = group; blk.ok; it += kNarrowGroups) {
             const uint32_t qs = it % QSTAGES, s = it % STAGES;
-            uint32_t hi[4], lo[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                split_scale(next[e], hi[e], lo[e]);
-            const uint4 own = make_uint4(
-                __byte_perm(hi[0], hi[1], 0x7632), __byte_perm(hi[2], hi[3], 0x7632),
-                __byte_perm(lo[0], lo[1], 0x7632), __byte_perm(lo[2], lo[3], 0x7632));
+            uint4 own;
+            split_scales(next[0], next[1], own.x, own.z);
+            split_scales(next[2], next[3], own.y, own.w);
             blk.advance(w, kNarrowGroups);
             fetch(); // the group's next k-block's, in flight while this one is converted
             if (!mbar_wait(bar_qfull + 8 * qs, (it / QSTAGES) & 1u, limit_ns))

@@ -34,11 +34,6 @@ def _codes(shape, f8, seed):
     return x.cuda().to(w8.FP8)
 
 
-def _bf16_part(s):
-    """The nearest bf16 (halves away from zero) of positive binary32 values."""
-    return ((s.view(torch.int32) + 0x8000) & ~0xFFFF).view(torch.float32)
-
-
 def _round_bf16(x):
     """Binary64 values rounded to eight significant bits, ties to even, in one step."""
     m, e = torch.frexp(x)
@@ -47,8 +42,8 @@ def _round_bf16(x):
 
 def _dequantized(q, s):
     """The bf16 operand s q as the kernels form it, in binary64: q hi + bf16(q lo), rounded."""
-    hi = _bf16_part(s)
-    lo = _bf16_part((s - hi).abs()) * torch.sign(s - hi)
+    hi = s.bfloat16().float()
+    lo = (s - hi).bfloat16().float()
     v = q.float().double()
     return _round_bf16(v * hi.double()[:, None] + _round_bf16(v * lo.double()[:, None]))
 
@@ -165,6 +160,24 @@ def test_extreme_codes_and_zero_scales():
     q8 = codes.view(w8.FP8).repeat(N, 1).contiguous()
     got = w8.w8a8_gemm_dgrad_fp8(dy, q8, s)
     assert torch.equal(got[0].float(), codes.view(w8.FP8).float() * 0.5)
+
+
+@pytest.mark.parametrize("name,M,N,K", [("dgrad", 16, 256, 272), ("dgrad", 200, 256, 272),
+                                        ("dgrad", 4100, 256, 272), ("wgrad", 64, 256, 272)])
+def test_a_broken_scale_or_gradient_is_not_hidden(name, M, N, K):
+    """A NaN (any payload) or infinite scale makes NaN of every sum it is in, in each form of the
+    kernel; a NaN in dy of its own row's sums only."""
+    rows = M if name == "wgrad" else N
+    fn = getattr(w8, "w8a8_gemm_" + name)
+    dy, q, s = _dy(M, N, 50), _codes((rows, K), False, 51), _scales(rows, 52)
+    for bits in (0x7FFFFFFF, 0x7FC00000, -1, 0x7F800000):
+        bad = s.clone()
+        bad.view(torch.int32)[7] = bits
+        assert fn(dy, q, bad).isnan().all()
+    dy[3, 5] = float("nan")
+    got = fn(dy, q, s).isnan()
+    hit = 5 if name == "wgrad" else 3
+    assert got[hit].all() and int(got.sum()) == K
 
 
 @pytest.mark.parametrize("name,M,N,K", [("dgrad", 40, 4096, 512), ("wgrad", 2100, 264, 272),
