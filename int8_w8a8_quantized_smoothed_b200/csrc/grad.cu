@@ -278,59 +278,91 @@ constexpr int64_t kGradNarrowRows = 128;
 // 256 rows (us, that form / this: 512 x 14336 x 4096 68 / 94, 2048 x 28672 x 4096 390 / 425,
 // 4096 x 8192 x 4096 225 / 212, 8192 x 4096 x 4096 213 / 185).
 constexpr int64_t kGradDequantRows = 4096;
+// The kernel that converts Q itself has tiles of 256 x 256, or of 512 x 256 with half the
+// conversions but nothing to hide a tile's end behind: a k-block of either, and that end, us.
+constexpr double kConvOneUs = 0.46, kConvTwoUs = 0.79, kTailUs = 5.0, kTailSiluUs = 8.0;
+// Operands of up to this many bytes stay in L2 (126 MB) from one use to the next.
+constexpr int64_t kGradL2Bytes = 64 << 20;
 
-// False when there are more tiles than an int counts.
-bool grad_plan(int64_t I, int64_t J, int64_t R, bool wgrad, int sms, GradPlan *p)
+// The tiles of one form and how many pairs (CTAs) share the last ones; returns the time, us.
+// The last tiles' k-blocks are split over more pairs where that saves more than the partial tiles
+// cost: a k-block takes `each` us and a tile's end `tail` us more, the second launch about 3 us, and
+// the partial tiles are stored and read at about 6 MB a us.
+// Equal parts of every tile, so that the pairs walk r together and find each other's rows of Q and
+// columns of dy in L2; uneven ones (all pairs busy, each at an r of its own) only where `uneven`
+// says that both operands stay in L2 anyway: 1024 x 28672 x 4096 took 256 us uneven over 74 pairs,
+// 219 us with 64 pairs of equal parts; 512 x 4096 x 14336 74 us uneven, 77 us without.
+double plan_tiles(GradWork *w, int64_t I, int64_t J, int64_t R, int tile_i, int tile_j, int br,
+                  int64_t pairs, double each, double tail, int min_share, bool uneven)
 {
-    GradWork *w = &p->w;
-    p->form = I >= kGradDequantRows ? kGradDequant
-              : !wgrad && I <= kGradNarrowRows ? kGradNarrow : kGradConv;
-    const bool narrow = p->form == kGradNarrow;
-    p->nt = I <= 16 ? 16 : I <= 32 ? 32 : I <= 64 ? 64 : 128;
-    w->tile_i = narrow ? p->nt : kGradTile;
-    w->tile_j = narrow ? 128 : kGradTile;
-    const int64_t ni = (I + w->tile_i - 1) / w->tile_i, nj = (J + w->tile_j - 1) / w->tile_j;
-    const int64_t br = narrow ? kNarrowBR : kGradBR;
-    const int64_t tiles = ni * nj, kb = (R + br - 1) / br;
-    const int64_t pairs = narrow ? sms : sms / 2;
-    if (tiles > (1 << 30))
-        return false;
+    const int64_t ni = (I + tile_i - 1) / tile_i, nj = (J + tile_j - 1) / tile_j;
+    const int64_t kb = (R + br - 1) / br, tiles = ni * nj;
     w->I = static_cast<int>(I);
     w->J = static_cast<int>(J);
     w->R = static_cast<int>(R);
+    w->tile_i = tile_i;
+    w->tile_j = tile_j;
     w->ni = static_cast<int>(ni);
     w->nj = static_cast<int>(nj);
     w->kblocks = static_cast<int>(kb);
-    w->group_i = 8;
+    w->group_i = tile_i > kGradTile ? 4 : 8;
     w->npairs = static_cast<int>(pairs);
     w->whole = static_cast<int>(tiles / pairs * pairs);
     w->rem = static_cast<int>(tiles % pairs);
-    // The last tiles' k-blocks are split over more pairs (CTAs) where that saves more time than the
-    // partial tiles cost: a k-block takes about 0.4 us (narrow), 0.5 us (converted by the kernel)
-    // or 0.35 us; the second launch about 3 us, and the partial tiles are stored and read at about
-    // 6 MB a us.
     w->rem_pairs = w->rem;
-    const double each = narrow ? 0.4 : p->form == kGradConv ? 0.5 : 0.35;
-    const double tile_bytes = 4.0 * std::min<int64_t>(I, w->tile_i) * w->tile_j;
-    double best = each * static_cast<double>(kb);
-    for (int k = 2; w->rem > 0 && k <= 65; ++k) {
-        const int64_t split =
-            std::min(pairs, static_cast<int64_t>(w->rem) * (k <= 64 ? k : pairs));
+    const double tile_bytes = 4.0 * std::min<int64_t>(I, tile_i) * tile_j;
+    const double whole = static_cast<double>(tiles / pairs) * (each * static_cast<double>(kb) + tail);
+    if (w->rem == 0)
+        return whole;
+    double best = each * static_cast<double>(kb) + tail;
+    for (int k = 2; k <= 65; ++k) {
+        int64_t split = static_cast<int64_t>(w->rem) * (k <= 64 ? k : pairs);
+        if (split > pairs && !uneven)
+            break;
+        split = std::min(pairs, split);
         const double share = static_cast<double>((w->rem * kb + split - 1) / split);
-        const double time = each * share + 3.0 + (split + w->rem) * tile_bytes * 2 / 6e6;
-        if (share >= (narrow ? 2 : 4) && time < best) {
+        const double time = each * share + tail + 3.0 + (split + w->rem) * tile_bytes * 2 / 6e6;
+        if (share >= min_share && time < best) {
             best = time;
             w->rem_pairs = static_cast<int>(split);
         }
         if (split == pairs)
             break;
     }
-    p->part_off = p->form == kGradDequant
-                      ? (static_cast<size_t>(R) * static_cast<size_t>(J) * 2 + 255) / 256 * 256
-                      : 0;
+    return whole + best;
+}
+
+// False when there are more tiles than an int counts.
+bool grad_plan(int64_t I, int64_t J, int64_t R, bool wgrad, bool silu, int sms, GradPlan *p)
+{
+    if ((I / kGradTile + 1) * (J / kGradTile + 1) > (1 << 30))
+        return false;
+    p->nt = I <= 16 ? 16 : I <= 32 ? 32 : I <= 64 ? 64 : 128;
+    p->part_off = 0;
+    const int pairs = sms / 2;
+    const bool dequant = I >= kGradDequantRows;
+    const bool in_l2 = 2 * I * R + (dequant ? 2 : 1) * R * J <= kGradL2Bytes;
+    if (dequant) {
+        p->form = kGradDequant;
+        plan_tiles(&p->w, I, J, R, kGradTile, kGradTile, kGradBR, pairs, 0.35, 0.0, 4, in_l2);
+        p->part_off = (static_cast<size_t>(R) * static_cast<size_t>(J) * 2 + 255) / 256 * 256;
+    } else if (!wgrad && I <= kGradNarrowRows) {
+        p->form = kGradNarrow; // every CTA streams codes of its own
+        plan_tiles(&p->w, I, J, R, p->nt, 128, kNarrowBR, sms, 0.4, 0.0, 2, true);
+    } else {
+        p->form = kGradConv;
+        GradWork two;
+        const double t1 = plan_tiles(&p->w, I, J, R, kGradTile, kGradTile, kGradBR, pairs,
+                                     kConvOneUs, 0.0, 4, in_l2);
+        const double t2 = plan_tiles(&two, I, J, R, 2 * kGradTile, kGradTile, kGradBR, pairs,
+                                     kConvTwoUs, silu ? kTailSiluUs : kTailUs, 4, in_l2);
+        if (t2 < t1)
+            p->w = two;
+    }
     p->ws_bytes = p->part_off;
-    if (w->rem_pairs > w->rem)
-        p->ws_bytes += static_cast<size_t>(w->rem_pairs) * 2 * w->tile_i * w->tile_j * sizeof(float);
+    if (p->w.rem_pairs > p->w.rem)
+        p->ws_bytes +=
+            static_cast<size_t>(p->w.rem_pairs) * 2 * p->w.tile_i * p->w.tile_j * sizeof(float);
     return true;
 }
 
@@ -367,13 +399,13 @@ int launch_fixup(const GradWork &w, const float *part, const uint16_t *gate_up, 
                          st, w, part, gate_up, out);
 }
 
-template <bool CONV, bool WGRAD, bool F8, bool SILU>
+template <bool CONV, int H, bool WGRAD, bool F8, bool SILU>
 int launch_grad(const CUtensorMap &ta, const CUtensorMap &tq, const float *scale,
                 const GradWork &w, const uint16_t *gate_up, uint16_t *out, float *part, int dev,
                 cudaStream_t st)
 {
-    using Cfg = GradCfg<CONV>;
-    auto kernel = grad_gemm_kernel<CONV, WGRAD, F8, SILU>;
+    using Cfg = GradCfg<CONV, H>;
+    auto kernel = grad_gemm_kernel<CONV, H, WGRAD, F8, SILU>;
     if (int rc = ensure_smem(reinterpret_cast<const void *>(kernel), dev, Cfg::kSmemBytes))
         return rc;
     const unsigned pairs = static_cast<unsigned>(w.whole > 0 ? w.npairs : w.rem_pairs);
@@ -382,6 +414,16 @@ int launch_grad(const CUtensorMap &ta, const CUtensorMap &tq, const float *scale
                                        part, kWaitLimitNs))
         return rc;
     return launch_fixup<SILU>(w, part, gate_up, out, dev, st);
+}
+
+template <bool WGRAD, bool F8, bool SILU>
+int launch_conv(const CUtensorMap &ta, const CUtensorMap &tq, const float *scale,
+                const GradWork &w, const uint16_t *gate_up, uint16_t *out, float *part, int dev,
+                cudaStream_t st)
+{
+    return w.tile_i > kGradTile
+               ? launch_grad<true, 2, WGRAD, F8, SILU>(ta, tq, scale, w, gate_up, out, part, dev, st)
+               : launch_grad<true, 1, WGRAD, F8, SILU>(ta, tq, scale, w, gate_up, out, part, dev, st);
 }
 
 template <int NT, bool F8, bool SILU>
@@ -448,7 +490,7 @@ int grad_impl(bool f8, const uint16_t *dy, const void *q, const float *scale, in
         return rc;
     const int64_t R = WGRAD ? M : N;
     GradPlan p;
-    if (!grad_plan(WGRAD ? N : M, K, R, WGRAD, sms, &p))
+    if (!grad_plan(WGRAD ? N : M, K, R, WGRAD, SILU, sms, &p))
         return W8A8_ERR_UNSUPPORTED_SHAPE;
     if (p.ws_bytes > 0 && (workspace == nullptr || workspace_bytes < p.ws_bytes))
         return W8A8_ERR_WORKSPACE;
@@ -468,10 +510,8 @@ int grad_impl(bool f8, const uint16_t *dy, const void *q, const float *scale, in
                                                          part, dev, st)
                           : launch_narrow_nt<false, SILU>(p.nt, ta, tq, scale, p.w, gate_up, out,
                                                           part, dev, st);
-        return f8 ? launch_grad<true, WGRAD, true, SILU>(ta, tq, scale, p.w, gate_up, out, part,
-                                                         dev, st)
-                  : launch_grad<true, WGRAD, false, SILU>(ta, tq, scale, p.w, gate_up, out, part,
-                                                          dev, st);
+        return f8 ? launch_conv<WGRAD, true, SILU>(ta, tq, scale, p.w, gate_up, out, part, dev, st)
+                  : launch_conv<WGRAD, false, SILU>(ta, tq, scale, p.w, gate_up, out, part, dev, st);
     }
     uint16_t *b = static_cast<uint16_t *>(workspace);
     if (encode_grad(&tq, b, R, K, 2, kGradBR, true))
@@ -479,7 +519,7 @@ int grad_impl(bool f8, const uint16_t *dy, const void *q, const float *scale, in
     if ((rc = f8 ? launch_dequant<true>(q, scale, R, K, b, dev, sms, st)
                  : launch_dequant<false>(q, scale, R, K, b, dev, sms, st)))
         return rc;
-    return launch_grad<false, WGRAD, false, SILU>(ta, tq, scale, p.w, gate_up, out, part, dev, st);
+    return launch_grad<false, 1, WGRAD, false, SILU>(ta, tq, scale, p.w, gate_up, out, part, dev, st);
 }
 
 size_t grad_workspace(int64_t M, int64_t N, int64_t K, bool wgrad)
@@ -489,8 +529,13 @@ size_t grad_workspace(int64_t M, int64_t N, int64_t K, bool wgrad)
     int dev, sms = 148;
     if (current_device(&dev, &sms))
         sms = 148;
-    GradPlan p;
-    return grad_plan(wgrad ? N : M, K, wgrad ? M : N, wgrad, sms, &p) ? p.ws_bytes : 0;
+    GradPlan p, q;
+    if (!grad_plan(wgrad ? N : M, K, wgrad ? M : N, wgrad, false, sms, &p))
+        return 0;
+    if (wgrad)
+        return p.ws_bytes;
+    grad_plan(M, K, N, false, true, sms, &q); // one size serves the input gradient's two forms
+    return std::max(p.ws_bytes, q.ws_bytes);
 }
 
 } // namespace

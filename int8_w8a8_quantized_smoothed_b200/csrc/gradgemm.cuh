@@ -23,12 +23,9 @@
 
 namespace w8a8 {
 
-// warps: 0 A producer, 1 MMA, 2 Q producer (CONV); 4 .. 7 epilogue; 8 .. 23 converters (CONV)
-constexpr int kGradThreads = 768;
+// warps: 0 A producer, 1 MMA, 2 Q producer (CONV); 4 .. 7 epilogue; from 8 on converters (CONV)
 constexpr int kGradConvWarp0 = 8;
-constexpr int kGradConvWarps = 16;
-constexpr int kGradConvGroups = 4; // groups of converter warps, each on its own k-block
-constexpr int kGradTile = 256; // rows i and columns j of a pair's tile
+constexpr int kGradTile = 256; // columns j of a pair's tile, and rows i (of each half, if two)
 constexpr int kGradBR = 64;    // r per k-block: one 128-byte row of bf16
 
 // Tiles [0, whole) go to the pairs one after another; the remaining tiles' k-blocks are split
@@ -102,15 +99,19 @@ struct GradBlocks {
 };
 
 // CONV: the kernel converts Q itself; otherwise B is a bf16 matrix loaded like A.
-template <bool CONV> struct GradCfg {
-    static constexpr int STAGES = CONV ? 4 : 6;
-    static constexpr int QSTAGES = CONV ? 8 : 0; // two a group: one is loaded meanwhile
+// H: the tile's halves of 256 rows i, both multiplied by the same converted tile of B.
+template <bool CONV, int H> struct GradCfg {
+    static_assert(H == 1 || (H == 2 && CONV), "halves");
+    static constexpr int GROUPS = H == 2 ? 3 : 4; // of converter warps, each on its own k-block
+    static constexpr int GROUP_WARPS = 4;
+    static constexpr int STAGES = H == 2 ? 3 : CONV ? 4 : 6;
+    static constexpr int QSTAGES = CONV ? 2 * GROUPS : 0; // two a group: one is loaded meanwhile
     // A converter group meets a stage of either ring again only after it has used it before (see
     // the narrow kernel's).
-    static_assert(QSTAGES % kGradConvGroups == 0 && (!CONV || STAGES % kGradConvGroups == 0),
-                  "rings and groups");
-    static constexpr int kThreads = CONV ? kGradThreads : 256; // without: no converter warps
-    static constexpr int kABytes = 128 * kGradBR * 2;
+    static_assert(QSTAGES % GROUPS == 0 && (!CONV || STAGES % GROUPS == 0), "rings and groups");
+    static constexpr int kThreads = (kGradConvWarp0 + (CONV ? GROUPS * GROUP_WARPS : 0)) * 32;
+    static constexpr int kHalfBytes = 128 * kGradBR * 2;
+    static constexpr int kABytes = H * kHalfBytes;
     static constexpr int kBBytes = 128 * kGradBR * 2;
     static constexpr int kQBytes = 128 * kGradBR;
     static constexpr int kBOff = STAGES * kABytes;
@@ -120,7 +121,8 @@ template <bool CONV> struct GradCfg {
     // full[S], empty[S], qfull[QS], qempty[QS], tfull[2], tempty[2], tensor-memory slot
     static constexpr int kSmemBytes = kBarOff + (2 * STAGES + 2 * QSTAGES + 6) * 8 + 16 + 1024;
     static_assert(kSmemBytes <= 232448, "shared memory per CTA");
-    static constexpr int kTmemCols = 512; // two 128 x 256 accumulators per CTA
+    // two 128 x 256 accumulators per CTA: of two tiles by turns, or of a tile's halves
+    static constexpr int kTmemCols = 512;
 };
 
 // 256-row bf16 MMA over the pair (see umma_i8_pair).
@@ -363,18 +365,19 @@ __device__ __forceinline__ void stage_store(const uint4 *stage, int lane, char *
     }
 }
 
-// A CTA pair per 256 x 256 tile (cta_group::2): each CTA holds 128 rows of A and 128 columns of B
-// and accumulates 128 x 256. WGRAD: A is MN-major. SILU: the epilogue turns C = da into dg and du
+// A CTA pair per 256 H x 256 tile (cta_group::2): each CTA holds 128 rows of A a half and 128
+// columns of B and accumulates 128 x 256 a half. WGRAD: A is MN-major. SILU: the epilogue turns C = da into dg and du
 // (out is [I, 2J]) with the forward call's gate|up values.
-template <bool CONV, bool WGRAD, bool F8, bool SILU>
-__global__ void __launch_bounds__(GradCfg<CONV>::kThreads, 1)
+template <bool CONV, int H, bool WGRAD, bool F8, bool SILU>
+__global__ void __launch_bounds__(GradCfg<CONV, H>::kThreads, 1)
     grad_gemm_kernel(const __grid_constant__ CUtensorMap tmA,
                      const __grid_constant__ CUtensorMap tmQ, const float *__restrict__ scale,
                      const GradWork w, const uint16_t *__restrict__ gate_up,
                      uint16_t *__restrict__ out, float *__restrict__ part,
                      unsigned long long limit_ns)
 {
-    using Cfg = GradCfg<CONV>;
+    using Cfg = GradCfg<CONV, H>;
+    constexpr int kTileI = H * kGradTile;
     constexpr int STAGES = Cfg::STAGES, QSTAGES = CONV ? Cfg::QSTAGES : 1;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>(
@@ -395,12 +398,12 @@ __global__ void __launch_bounds__(GradCfg<CONV>::kThreads, 1)
     if (threadIdx.x == 0) {
         for (int s = 0; s < STAGES; ++s) {
             // the loads' bytes, and the group of converters of each CTA
-            mbar_init(bar_full + 8 * s, CONV ? 1 + 2 * kGradConvWarps / kGradConvGroups : 1);
+            mbar_init(bar_full + 8 * s, CONV ? 1 + 2 * Cfg::GROUP_WARPS : 1);
             mbar_init(bar_empty + 8 * s, 1);
         }
         for (int s = 0; CONV && s < QSTAGES; ++s) {
             mbar_init(bar_qfull + 8 * s, 1);
-            mbar_init(bar_qempty + 8 * s, kGradConvWarps / kGradConvGroups);
+            mbar_init(bar_qempty + 8 * s, Cfg::GROUP_WARPS);
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(bar_tfull + 8 * b, 1);
@@ -434,7 +437,7 @@ __global__ void __launch_bounds__(GradCfg<CONV>::kThreads, 1)
         while (ok && walk.next(w, sg)) {
             int ib, jb;
             tile_coords(sg.tile, w.ni, w.nj, w.group_i, ib, jb);
-            const int i0 = ib * kGradTile + static_cast<int>(rank) * 128;
+            const int i0 = ib * kTileI + static_cast<int>(rank) * 128;
             const int j0 = jb * kGradTile + static_cast<int>(rank) * 128;
             int r0 = sg.kb0 * kGradBR;
             for (int n = sg.kb1 - sg.kb0; n > 0; --n, ++it, r0 += kGradBR) {
@@ -447,12 +450,16 @@ __global__ void __launch_bounds__(GradCfg<CONV>::kThreads, 1)
                     if (rank == 0)
                         mbar_expect_tx(bar_full + 8 * ring.s,
                                        2 * (Cfg::kABytes + (CONV ? 0 : Cfg::kBBytes)));
-                    const uint32_t dst = sA + ring.s * Cfg::kABytes;
-                    if constexpr (WGRAD) {
-                        tma_load_2d_pair(dst, &tmA, full, i0, r0);
-                        tma_load_2d_pair(dst + 8192, &tmA, full, i0 + 64, r0);
-                    } else {
-                        tma_load_2d_pair(dst, &tmA, full, r0, i0);
+#pragma unroll
+                    for (int h = 0; h < H; ++h) {
+                        const uint32_t dst = sA + ring.s * Cfg::kABytes + h * Cfg::kHalfBytes;
+                        const int i = i0 + h * kGradTile;
+                        if constexpr (WGRAD) {
+                            tma_load_2d_pair(dst, &tmA, full, i, r0);
+                            tma_load_2d_pair(dst + 8192, &tmA, full, i + 64, r0);
+                        } else {
+                            tma_load_2d_pair(dst, &tmA, full, r0, i);
+                        }
                     }
                     if constexpr (!CONV) {
                         const uint32_t b = sB + ring.s * Cfg::kBBytes;
@@ -477,14 +484,21 @@ __global__ void __launch_bounds__(GradCfg<CONV>::kThreads, 1)
             constexpr uint32_t kStepA = (WGRAD ? 2048 : 32) / 16, kStepB = 2048 / 16;
             bool ok = true;
             Ring<STAGES> ring;
+            // with one half the two accumulators take turns; with two each has its own
             Ring<2> acc;
+            uint32_t tile_ph = 0;
             GradWalk walk(w, pair);
             GradSegment sg;
-            while (ok && walk.next(w, sg)) {
-                if (!mbar_wait_cluster(bar_tempty + 8 * acc.s, acc.ph ^ 1u, limit_ns))
-                    break;
+            auto free_acc = [&](int h) { // its last tile has been read out
+                const uint32_t b = H == 2 ? h : acc.s, ph = H == 2 ? tile_ph : acc.ph;
+                const bool got = mbar_wait_cluster(bar_tempty + 8 * b, ph ^ 1u, limit_ns);
                 tc_fence_after();
-                const uint32_t d = tmem_base + acc.s * kGradTile;
+                return got;
+            };
+            while (ok && walk.next(w, sg)) {
+                if (!free_acc(0))
+                    break;
+                const uint32_t d = tmem_base + (H == 2 ? 0 : acc.s) * kGradTile;
                 uint32_t accumulate = 0;
                 for (int n = sg.kb1 - sg.kb0; n > 0; --n) {
                     if (!mbar_wait_cluster(bar_full + 8 * ring.s, ring.ph, limit_ns)) {
@@ -492,23 +506,37 @@ __global__ void __launch_bounds__(GradCfg<CONV>::kThreads, 1)
                         break;
                     }
                     tc_fence_after();
-                    if (lane == 0) {
-                        const uint64_t a0 = da + ring.s * (Cfg::kABytes / 16);
-                        const uint64_t b0 = db + ring.s * (Cfg::kBBytes / 16);
 #pragma unroll
-                        for (int k = 0; k < kGradBR / 16; ++k)
-                            umma_bf16_pair(d, a0 + k * kStepA, b0 + k * kStepB, idesc,
-                                           k > 0 ? 1u : accumulate);
-                        umma_commit_pair(bar_empty + 8 * ring.s, 0x3);
+                    for (int h = 0; h < H; ++h) {
+                        if (h == 1 && !accumulate && !free_acc(1)) {
+                            ok = false;
+                            break;
+                        }
+                        if (lane == 0) {
+                            const uint64_t a0 = da + ring.s * (Cfg::kABytes / 16) +
+                                                h * (Cfg::kHalfBytes / 16);
+                            const uint64_t b0 = db + ring.s * (Cfg::kBBytes / 16);
+#pragma unroll
+                            for (int k = 0; k < kGradBR / 16; ++k)
+                                umma_bf16_pair(d + h * kGradTile, a0 + k * kStepA,
+                                               b0 + k * kStepB, idesc, k > 0 ? 1u : accumulate);
+                            if (h == H - 1)
+                                umma_commit_pair(bar_empty + 8 * ring.s, 0x3);
+                            if (H == 2 && n == 1)
+                                umma_commit_pair(bar_tfull + 8 * h, 0x3);
+                        }
+                        __syncwarp();
                     }
-                    __syncwarp();
+                    if (!ok)
+                        break;
                     accumulate = 1;
                     ring.next();
                 }
-                if (ok && lane == 0)
+                if (H == 1 && ok && lane == 0)
                     umma_commit_pair(bar_tfull + 8 * acc.s, 0x3);
                 __syncwarp();
                 acc.next();
+                tile_ph ^= 1u;
             }
         }
     } else if (warp >= 4 && warp < 8) {
@@ -523,95 +551,102 @@ __global__ void __launch_bounds__(GradCfg<CONV>::kThreads, 1)
         while (walk.next(w, sg)) {
             int ib, jb;
             tile_coords(sg.tile, w.ni, w.nj, w.group_i, ib, jb);
-            const uint32_t buf = seg & 1u, aph = (seg >> 1) & 1u;
-            ++seg;
-            const int row0 = ib * kGradTile + static_cast<int>(rank) * 128 + quarter * 32;
-            const int rows = min(32, w.I - row0); // may be negative: nothing stored
-            const int64_t ld = static_cast<int64_t>(w.J) * (SILU ? 4 : 2); // bytes
-            float *slot = part + ((static_cast<int64_t>(pair) * 2 + sg.slot) * kGradTile +
-                                  rank * 128 + quarter * 32) * kGradTile;
-            // SILU: the gate and up values of a chunk of 32 columns are on their way while the
-            // chunk before it is worked on, the first ones while the tile is still multiplied
-            auto fetch = [&](int c) {
-                const int j0 = jb * kGradTile + c * 32;
-                const char *gu = reinterpret_cast<const char *>(gate_up) + row0 * ld + j0 * 2;
-                const int bytes = min(64, (w.J - j0) * 2);
-                uint4 *to = stage_w + (c & 1) * 256;
-                stage_load<4>(to, lane, gu, ld, rows, bytes);
-                stage_load<4>(to + 128, lane, gu + static_cast<int64_t>(w.J) * 2, ld, rows, bytes);
-                stage_load_commit();
-            };
-            if constexpr (SILU)
-                if (!sg.partial)
-                    fetch(0);
-            if (!mbar_wait(bar_tfull + 8 * buf, aph, limit_ns))
-                break;
-            __syncwarp();
-            tc_fence_after();
-            const uint32_t tbase =
-                tmem_base + buf * kGradTile + (static_cast<uint32_t>(quarter * 32) << 16);
+            bool ok = true;
 #pragma unroll 1
-            for (int c = 0; c < kGradTile / 32; ++c) {
-                const int j0 = jb * kGradTile + c * 32;
-                uint32_t r[32];
-                if constexpr (SILU)
-                    if (!sg.partial && c + 1 < kGradTile / 32)
-                        fetch(c + 1);
-                tmem_ld_32x32b_x32(tbase + c * 32, r);
-                tmem_ld_wait();
-                if (sg.partial) {
-#pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        stage_w[stage_at<8>(lane, j)] =
-                            make_uint4(r[4 * j], r[4 * j + 1], r[4 * j + 2], r[4 * j + 3]);
-                    __syncwarp();
-                    stage_store<8>(stage_w, lane, reinterpret_cast<char *>(slot + c * 32),
-                                   kGradTile * 4, rows, 128);
-                } else if constexpr (SILU) {
-                    if (c + 1 < kGradTile / 32)
-                        stage_load_wait<1>();
-                    else
-                        stage_load_wait<0>();
-                    __syncwarp();
-                    uint4 *st = stage_w + (c & 1) * 256;
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) { // the lane's own row, in place
-                        float da[8];
-#pragma unroll
-                        for (int i = 0; i < 8; ++i)
-                            da[i] = __uint_as_float(r[e * 8 + i]);
-                        uint4 *g = st + stage_at<4>(lane, e);
-                        silu_grad8(da, g[0], g[128], g[0], g[128]);
-                    }
-                    __syncwarp();
-                    char *dst = reinterpret_cast<char *>(out) + row0 * ld + j0 * 2;
+            for (int h = 0; h < H && ok; ++h) {
+                const uint32_t buf = H == 2 ? h : seg & 1u, aph = (H == 2 ? seg : seg >> 1) & 1u;
+                const int row0 = ib * kTileI + h * kGradTile + static_cast<int>(rank) * 128 + quarter * 32;
+                const int rows = min(32, w.I - row0); // may be negative: nothing stored
+                const int64_t ld = static_cast<int64_t>(w.J) * (SILU ? 4 : 2); // bytes
+                float *slot = part + ((static_cast<int64_t>(pair) * 2 + sg.slot) * kTileI +
+                                      h * kGradTile + rank * 128 + quarter * 32) * kGradTile;
+                // SILU: the gate and up values of a chunk of 32 columns are on their way while the
+                // chunk before it is worked on, the first ones while the tile is still multiplied
+                auto fetch = [&](int c) {
+                    const int j0 = jb * kGradTile + c * 32;
+                    const char *gu = reinterpret_cast<const char *>(gate_up) + row0 * ld + j0 * 2;
                     const int bytes = min(64, (w.J - j0) * 2);
-                    stage_store<4>(st, lane, dst, ld, rows, bytes);
-                    stage_store<4>(st + 128, lane, dst + static_cast<int64_t>(w.J) * 2, ld, rows,
-                                   bytes);
-                } else { // two chunks of columns go out together, 128 bytes a row
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const uint32_t *f = &r[e * 8];
-                        stage_w[stage_at<8>(lane, (c & 1) * 4 + e)] = make_uint4(
-                            pack_bf16x2(__uint_as_float(f[0]), __uint_as_float(f[1])),
-                            pack_bf16x2(__uint_as_float(f[2]), __uint_as_float(f[3])),
-                            pack_bf16x2(__uint_as_float(f[4]), __uint_as_float(f[5])),
-                            pack_bf16x2(__uint_as_float(f[6]), __uint_as_float(f[7])));
-                    }
-                    if (c & 1) {
-                        __syncwarp();
-                        stage_store<8>(stage_w, lane,
-                                       reinterpret_cast<char *>(out) + row0 * ld + (j0 - 32) * 2, ld,
-                                       rows, min(128, (w.J - j0 + 32) * 2));
-                    }
-                }
+                    uint4 *to = stage_w + (c & 1) * 256;
+                    stage_load<4>(to, lane, gu, ld, rows, bytes);
+                    stage_load<4>(to + 128, lane, gu + static_cast<int64_t>(w.J) * 2, ld, rows, bytes);
+                    stage_load_commit();
+                };
+                if constexpr (SILU)
+                    if (!sg.partial)
+                        fetch(0);
+                ok = mbar_wait(bar_tfull + 8 * buf, aph, limit_ns);
+                if (!ok)
+                    break;
                 __syncwarp();
+                tc_fence_after();
+                const uint32_t tbase =
+                    tmem_base + buf * kGradTile + (static_cast<uint32_t>(quarter * 32) << 16);
+#pragma unroll 1
+                for (int c = 0; c < kGradTile / 32; ++c) {
+                    const int j0 = jb * kGradTile + c * 32;
+                    uint32_t r[32];
+                    if constexpr (SILU)
+                        if (!sg.partial && c + 1 < kGradTile / 32)
+                            fetch(c + 1);
+                    tmem_ld_32x32b_x32(tbase + c * 32, r);
+                    tmem_ld_wait();
+                    if (sg.partial) {
+#pragma unroll
+                        for (int j = 0; j < 8; ++j)
+                            stage_w[stage_at<8>(lane, j)] =
+                                make_uint4(r[4 * j], r[4 * j + 1], r[4 * j + 2], r[4 * j + 3]);
+                        __syncwarp();
+                        stage_store<8>(stage_w, lane, reinterpret_cast<char *>(slot + c * 32),
+                                       kGradTile * 4, rows, 128);
+                    } else if constexpr (SILU) {
+                        if (c + 1 < kGradTile / 32)
+                            stage_load_wait<1>();
+                        else
+                            stage_load_wait<0>();
+                        __syncwarp();
+                        uint4 *st = stage_w + (c & 1) * 256;
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) { // the lane's own row, in place
+                            float da[8];
+#pragma unroll
+                            for (int i = 0; i < 8; ++i)
+                                da[i] = __uint_as_float(r[e * 8 + i]);
+                            uint4 *g = st + stage_at<4>(lane, e);
+                            silu_grad8(da, g[0], g[128], g[0], g[128]);
+                        }
+                        __syncwarp();
+                        char *dst = reinterpret_cast<char *>(out) + row0 * ld + j0 * 2;
+                        const int bytes = min(64, (w.J - j0) * 2);
+                        stage_store<4>(st, lane, dst, ld, rows, bytes);
+                        stage_store<4>(st + 128, lane, dst + static_cast<int64_t>(w.J) * 2, ld, rows,
+                                       bytes);
+                    } else { // two chunks of columns go out together, 128 bytes a row
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const uint32_t *f = &r[e * 8];
+                            stage_w[stage_at<8>(lane, (c & 1) * 4 + e)] = make_uint4(
+                                pack_bf16x2(__uint_as_float(f[0]), __uint_as_float(f[1])),
+                                pack_bf16x2(__uint_as_float(f[2]), __uint_as_float(f[3])),
+                                pack_bf16x2(__uint_as_float(f[4]), __uint_as_float(f[5])),
+                                pack_bf16x2(__uint_as_float(f[6]), __uint_as_float(f[7])));
+                        }
+                        if (c & 1) {
+                            __syncwarp();
+                            stage_store<8>(stage_w, lane,
+                                           reinterpret_cast<char *>(out) + row0 * ld + (j0 - 32) * 2, ld,
+                                           rows, min(128, (w.J - j0 + 32) * 2));
+                        }
+                    }
+                    __syncwarp();
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive_cluster(tempty0 + 8 * buf); // the leader's accumulator is free
             }
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0)
-                mbar_arrive_cluster(tempty0 + 8 * buf); // the leader's accumulator is free
+            if (!ok)
+                break;
+            ++seg;
         }
     } else if (CONV && warp == 2) {
         pdl_wait();
@@ -641,14 +676,14 @@ __global__ void __launch_bounds__(GradCfg<CONV>::kThreads, 1)
         if (ok)
             drain_ring(bar_qempty, it, QSTAGES, limit_ns);
     } else if (CONV && warp >= kGradConvWarp0) {
-        // converters: group g (four warps) takes every kGradConvGroups-th k-block, so the waits,
+        // converters: group g (four warps) takes every GROUPS-th k-block, so the waits,
         // loads and fences of several k-blocks overlap. Two threads share a row r of the
         // k-block's [64 r][128 j] codes, every other 16-byte piece each, starting at the lane's
         // own, so that eight lanes of a load, or of a store into the swizzled bf16 tile, fill all
         // banks.
         pdl_wait();
         constexpr int kGroupThreads = 2 * kGradBR;
-        static_assert(kGradConvWarps * 32 == kGradConvGroups * kGroupThreads, "two threads a row");
+        static_assert(Cfg::GROUP_WARPS * 32 == kGroupThreads, "two threads a row");
         const int ct = threadIdx.x - kGradConvWarp0 * 32;
         const int group = ct / kGroupThreads;
         const int row = ct % kGradBR, half = ct / kGradBR & 1;
@@ -661,7 +696,7 @@ __global__ void __launch_bounds__(GradCfg<CONV>::kThreads, 1)
         GradBlocks blk(w, pair, group);
         if (blk.ok)
             fetch(blk.kb);
-        for (uint32_t it = group; blk.ok; it += kGradConvGroups) {
+        for (uint32_t it = group; blk.ok; it += Cfg::GROUPS) {
             const RowScale sc = row_scale(next);
             const uint32_t qs = it % QSTAGES, s = it % STAGES;
             if (!mbar_wait(bar_qfull + 8 * qs, (it / QSTAGES) & 1u, limit_ns))
@@ -696,7 +731,7 @@ __global__ void __launch_bounds__(GradCfg<CONV>::kThreads, 1)
                 mbar_arrive(bar_qempty + 8 * qs);
             }
             // the scale of the group's next k-block, after the fence, which would wait for it
-            blk.advance(w, kGradConvGroups);
+            blk.advance(w, Cfg::GROUPS);
             if (blk.ok)
                 fetch(blk.kb);
         }
