@@ -273,13 +273,18 @@ struct GradPlan {
 
 // Up to this many rows i an input gradient runs the narrow kernel.
 constexpr int64_t kGradNarrowRows = 128;
-// From this many rows i on, Q is converted once ahead of the product: a pass over Q of 3 bytes a
-// code, after which the GEMM is free of the conversions that the other form makes again for every
-// 256 rows (us, that form / this: 512 x 14336 x 4096 68 / 94, 2048 x 28672 x 4096 390 / 425,
-// 4096 x 8192 x 4096 225 / 212, 8192 x 4096 x 4096 213 / 185).
-constexpr int64_t kGradDequantRows = 4096;
+// From this many rows i on and for sums of fewer than kGradDequantSum terms, Q is converted once
+// ahead of the product: a pass over Q of 3 bytes a code, after which the GEMM is free of the
+// conversions that the other form makes again for every 512 rows, and of that form's tile ends with
+// nothing to hide behind. With longer sums the two take the same time and the pass would only cost
+// its workspace (us, converting in the kernel / ahead: 4096 x 2048 x 4096 62 / 54, 8192 x 4096 x
+// 4096 218 / 186, 4096 x 8192 x 4096 207 / 208, 4096 x 28672 x 4096 sustained 804 / 820;
+// 2048 x 28672 x 4096 349 / 425).
+constexpr int64_t kGradDequantRows = 4096, kGradDequantSum = 8192;
 // The kernel that converts Q itself has tiles of 256 x 256, or of 512 x 256 with half the
-// conversions but nothing to hide a tile's end behind: a k-block of either, and that end, us.
+// conversions but nothing to hide a tile's end behind: a k-block of either, and that end, us. (By
+// 512 x 256 / 256 x 256: 2048 x 28672 x 4096 349 / 390 us, 2048 x 4096 x 4096 55 / 61, sustained
+// 394 / 447 and 55 / 62; wgrad 1024 x 4000 x 4096 38 / 35, silu 512 x 4096 x 14336 77 / 74.)
 constexpr double kConvOneUs = 0.46, kConvTwoUs = 0.79, kTailUs = 5.0, kTailSiluUs = 8.0;
 // Operands of up to this many bytes stay in L2 (126 MB) from one use to the next.
 constexpr int64_t kGradL2Bytes = 64 << 20;
@@ -340,7 +345,7 @@ bool grad_plan(int64_t I, int64_t J, int64_t R, bool wgrad, bool silu, int sms, 
     p->nt = I <= 16 ? 16 : I <= 32 ? 32 : I <= 64 ? 64 : 128;
     p->part_off = 0;
     const int pairs = sms / 2;
-    const bool dequant = I >= kGradDequantRows;
+    const bool dequant = I >= kGradDequantRows && R < kGradDequantSum;
     const bool in_l2 = 2 * I * R + (dequant ? 2 : 1) * R * J <= kGradL2Bytes;
     if (dequant) {
         p->form = kGradDequant;

@@ -18,11 +18,15 @@ pytestmark = pytest.mark.gpu
 
 # (M, N, K): single tokens, the smallest sides, sides that end inside a tile and inside a k-block,
 # sums split over the SMs (few tiles), whole waves of tiles with and without a remainder; rows that
-# the kernel dequantizes itself (fewer than 4096 of them) and that a pass before it does
+# the kernel dequantizes itself, in tiles of 256 and of 512 of them, and that a pass before it does
+# (4096 and more, sums of fewer than 8192)
 SHAPES = [(1, 8, 16), (1, 4096, 4096), (16, 6144, 512), (3, 72, 48), (64, 64, 64), (65, 56, 272),
           (300, 264, 528), (257, 1032, 4112), (2304, 512, 2304), (2304, 1024, 2304),
           (1000, 2056, 1040), (129, 14336, 256), (4100, 264, 528), (4100, 8200, 272),
-          (33, 4104, 4112), (100, 6144, 528), (128, 1000, 2064), (20, 640, 19072)]
+          (33, 4104, 4112), (100, 6144, 528), (128, 1000, 2064), (20, 640, 19072),
+          (769, 8200, 4112), (265, 7880, 4400), (263, 7576, 4416), (1309, 2504, 4112),
+          (3345, 2568, 4432), (3139, 10256, 528), (1282, 3976, 4656), (2570, 1312, 4112),
+          (2499, 3176, 4640)]
 
 
 def _codes(shape, f8, seed):
@@ -183,6 +187,8 @@ def test_a_broken_scale_or_gradient_is_not_hidden(name, M, N, K):
 @pytest.mark.parametrize("name,M,N,K", [("dgrad", 40, 4096, 512), ("wgrad", 2100, 264, 272),
                                         ("dgrad_silu", 40, 4096, 512),
                                         ("dgrad_silu", 4100, 8200, 272),
+                                        ("dgrad_silu", 4100, 4104, 272),
+                                        ("dgrad", 265, 7880, 4400), ("dgrad_silu", 3139, 10256, 528),
                                         ("dgrad", 300, 4096, 512)])
 def test_repeatable_streams_and_graphs(name, M, N, K):
     """The same bits on every call (split sums included), on a side stream, with the caller's
@@ -231,7 +237,7 @@ def test_repeatable_streams_and_graphs(name, M, N, K):
 
 
 @pytest.mark.parametrize("M,N,K", [(16, 28672, 4096), (128, 14336, 4096), (512, 8192, 4096),
-                                   (4096, 4096, 2048)])
+                                   (4096, 4096, 2048), (2048, 12288, 4096)])
 def test_many_calls_back_to_back(M, N, K):
     """Long sums, one launch right after another (from a graph too): every form's load, convert
     and multiply rings run full and out of step, and each call gives the first one's bits."""
