@@ -178,10 +178,11 @@ def _arg(t, name, dtype, shape, index):
     return t.data_ptr()
 
 
-def _out(t, name, dtype, shape, index):
-    """(tensor, address) of an output: the caller's, checked, or a new one."""
+def _out(t, name, dtype, shape, like, index):
+    """(tensor, address) of an output: the caller's, checked, or a new one beside `like` (in about
+    half the host time of a torch.empty that is told its device)."""
     if t is None:
-        t = torch.empty(shape, dtype=dtype, device=index)
+        t = like.new_empty(shape, dtype=dtype)
         return t, t.data_ptr()
     return t, _arg(t, name, dtype, shape, index)
 
@@ -216,13 +217,13 @@ def _on_device(fn):
     return call
 
 
-def _scratch(workspace, nbytes, index):
+def _scratch(workspace, nbytes, like, index):
     """(address, size, the tensor) of the caller's workspace, or of a new one for this call alone:
     nothing is kept between calls, so calls on any streams and captured graphs cannot share it."""
     if workspace is None:
         if nbytes == 0:
             return None, 0, None
-        workspace = torch.empty(nbytes, dtype=torch.uint8, device=index)
+        workspace = like.new_empty(nbytes, dtype=torch.uint8)
         return workspace.data_ptr(), nbytes, workspace
     if isinstance(workspace, Workspace):
         workspace, _ = workspace.get(nbytes)
@@ -809,9 +810,9 @@ def _sandwich_quant(name, code, y, residual, gamma_smoothed, eps, gamma_post, ep
         raise TypeError("residual and gamma_smoothed must be torch.Tensors")
     kind, pgate = _gate_arg(gate, M, K, index)
     shape = (M, K)
-    h_out, ph = _out(h_out, "h_out", torch.bfloat16, shape, index)
-    q, pq = _out(q, "q", code, shape, index)
-    s_tok, ps = _out(s_tok, "s_tok", torch.float32, (M,), index)
+    h_out, ph = _out(h_out, "h_out", torch.bfloat16, shape, y, index)
+    q, pq = _out(q, "q", code, shape, y, index)
+    s_tok, ps = _out(s_tok, "s_tok", torch.float32, (M,), y, index)
     rc = getattr(lib(), name)(
         y.data_ptr(), _arg(residual, "residual", torch.bfloat16, shape, index),
         _arg(gamma_post, "gamma_post", torch.float32, (K,), index),
@@ -864,13 +865,14 @@ def w8a8_sandwich_rmsnorm_backward(dz, y, h, gamma_smoothed, eps, dh=None, gamma
     kind, pgate = _gate_arg(gate, M, K, index)
     L = lib()
     shape = (M, K)
-    dy, pdy = _out(dy, "dy", torch.bfloat16, shape, index)
-    dresidual, pdr = _out(dresidual, "dresidual", torch.bfloat16, shape, index)
-    dpre = torch.empty(K, dtype=torch.float32, device=index)
-    dpost = None if gamma_post is None else torch.empty(K, dtype=torch.float32, device=index)
+    dy, pdy = _out(dy, "dy", torch.bfloat16, shape, dz, index)
+    dresidual, pdr = _out(dresidual, "dresidual", torch.bfloat16, shape, dz, index)
+    dpre = dz.new_empty(K, dtype=torch.float32)
+    dpost = None if gamma_post is None else dz.new_empty(K, dtype=torch.float32)
     dgate = None if gate is None else torch.empty_like(gate)
     wptr, wbytes, keep = _scratch(
-        workspace, _size("w8a8_sandwich_rmsnorm_backward_workspace_size", index, M, K), index)
+        workspace, _size("w8a8_sandwich_rmsnorm_backward_workspace_size", index, M, K), dz,
+        index)
     rc = L.w8a8_sandwich_rmsnorm_backward(
         dz.data_ptr(), _arg(dh, "dh", torch.bfloat16, shape, index),
         _arg(y, "y", torch.bfloat16, shape, index), _arg(h, "h", torch.bfloat16, shape, index),
@@ -912,9 +914,9 @@ def _grad(name, code, dy, q, scale, rows, out, out_name, gate_up, workspace):
         shape = (M, 2 * K)
         extra = (_arg(gate_up, "gate_up", torch.bfloat16, shape, index),)
     L = lib()
-    out, pout = _out(out, out_name, torch.bfloat16, shape, index)
+    out, pout = _out(out, out_name, torch.bfloat16, shape, dy, index)
     size = "w8a8_gemm_dgrad_workspace_size" if rows else "w8a8_gemm_wgrad_workspace_size"
-    wptr, wbytes, keep = _scratch(workspace, _size(size, index, M, N, K), index)
+    wptr, wbytes, keep = _scratch(workspace, _size(size, index, M, N, K), dy, index)
     rc = getattr(L, name)(dy.data_ptr(), pq, ps, M, N, K, *extra, pout, wptr, wbytes,
                           _current_stream(index))
     if rc:

@@ -58,7 +58,9 @@ def test_workspace_sizes(L):
     assert wg(72, 4096, 4096) == 72 * 4096 * 2      # or the bf16 activations; short sums whole
     assert wg(4096, 256, 256) == 16 * tile
     # the bf16 operand (to 256 bytes), then the partial tiles of a split
-    assert d(4100, 8200, 272) == 8200 * 272 * 2 + 74 * tile
+    assert d(4100, 8184, 272) == 8184 * 272 * 2 + 68 * tile
+    assert d(4100, 8200, 272) == 68 * tile          # longer sums are converted by the kernel
+    assert d(265, 7880, 4400) == 72 * 2 * tile      # in tiles of 512 rows
 
 
 def test_binding_refuses_cpu_tensors():
