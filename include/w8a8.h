@@ -14,8 +14,8 @@
  *
  * Conventions for every call:
  *   - All tensor pointers are DEVICE pointers owned by the caller; row-major, contiguous.
- *     The library allocates no device memory in any call; it keeps one small device status
- *     word per device (see w8a8_device_status) and nothing else.
+ *     The library allocates no device memory in any call; it keeps two status words per
+ *     device (see w8a8_device_status) and nothing else.
  *   - Every call is asynchronous on `stream` (0 = legacy default stream). Host-detectable
  *     errors are returned before anything is launched; a launch failure returns
  *     W8A8_ERR_CUDA. Device-side problems (a bounded wait that ran out) are reported by
