@@ -284,7 +284,8 @@ constexpr int64_t kGradDequantRows = 4096, kGradDequantSum = 8192;
 // The kernel that converts Q itself has tiles of 256 x 256, or of 512 x 256 with half the
 // conversions but nothing to hide a tile's end behind: a k-block of either, and that end, us. (By
 // 512 x 256 / 256 x 256: 2048 x 28672 x 4096 349 / 390 us, 2048 x 4096 x 4096 55 / 61, sustained
-// 394 / 447 and 55 / 62; wgrad 1024 x 4000 x 4096 38 / 35, silu 512 x 4096 x 14336 77 / 74.)
+// 394 / 447 and 55 / 62; wgrad 1024 x 4000 x 4096 38 / 35, silu 512 x 4096 x 14336 77 / 74. Of 45
+// random shapes the plan came within 5% of the better height in 43, within 6% in all.)
 constexpr double kConvOneUs = 0.46, kConvTwoUs = 0.79, kTailUs = 5.0, kTailSiluUs = 8.0;
 // Operands of up to this many bytes stay in L2 (126 MB) from one use to the next.
 constexpr int64_t kGradL2Bytes = 64 << 20;

@@ -168,7 +168,8 @@ __device__ __forceinline__ uint64_t sw128_mnmajor_desc(uint32_t saddr)
 // Arrive on an mbarrier of either CTA of the pair (a cluster address). Release at CTA scope: what
 // it publishes are stores to this CTA's own shared memory, behind a proxy fence of every thread
 // that made them, for the pair's MMA. At cluster scope the arrival itself took about 2000 cycles,
-// which four groups of converters could not hide (2048 x 28672 x 4096 440 us, now 390).
+// which four groups of converters could not hide (2048 x 28672 x 4096 in tiles of 256 rows: 440 us,
+// without it 390).
 __device__ __forceinline__ void mbar_arrive_pair(uint32_t bar_cluster)
 {
     asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar_cluster) : "memory");
@@ -366,8 +367,11 @@ __device__ __forceinline__ void stage_store(const uint4 *stage, int lane, char *
 }
 
 // A CTA pair per 256 H x 256 tile (cta_group::2): each CTA holds 128 rows of A a half and 128
-// columns of B and accumulates 128 x 256 a half. WGRAD: A is MN-major. SILU: the epilogue turns C = da into dg and du
-// (out is [I, 2J]) with the forward call's gate|up values.
+// columns of B and accumulates 128 x 256 a half. WGRAD: A is MN-major. SILU: the epilogue turns
+// C = da into dg and du (out is [I, 2J]) with the forward call's gate|up values.
+// Bound by the power limit in long runs: 2048 x 28672 x 4096 takes 349 us = 1.38 PFLOP/s, sustained
+// 394 us at 1.57 GHz (the bare bf16 product by a library 316 and 351 us); a k-block of 512 rows
+// takes about 1250 cycles, of them 1024 of MMA.
 template <bool CONV, int H, bool WGRAD, bool F8, bool SILU>
 __global__ void __launch_bounds__(GradCfg<CONV, H>::kThreads, 1)
     grad_gemm_kernel(const __grid_constant__ CUtensorMap tmA,
