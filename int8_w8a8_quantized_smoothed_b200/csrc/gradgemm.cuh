@@ -165,14 +165,18 @@ __device__ __forceinline__ uint64_t sw128_mnmajor_desc(uint32_t saddr)
     return d;
 }
 
-// Arrive on an mbarrier of either CTA of the pair (a cluster address). Release at CTA scope: what
-// it publishes are stores to this CTA's own shared memory, behind a proxy fence of every thread
-// that made them, for the pair's MMA. At cluster scope the arrival itself took about 2000 cycles,
-// which four groups of converters could not hide (2048 x 28672 x 4096 in tiles of 256 rows: 440 us,
-// without it 390).
+// Arrive on an mbarrier of either CTA of the pair (a cluster address), for the pair's MMA, which is
+// issued in the even CTA and reads both CTAs' converted tiles. The release is at cluster scope, as
+// the odd CTA's stores are published to a thread outside it, but of stores to this CTA's shared
+// memory alone (each behind its own thread's proxy fence): a release of all of memory took about
+// 2000 cycles, which four groups of converters could not hide (2048 x 28672 x 4096 in tiles of 256
+// rows 440 us against 390), nor could a warp that passes the groups' arrivals on (in tiles of 512
+// rows 396 us; 349 with a release at CTA scope, too narrow, 342 with this one).
 __device__ __forceinline__ void mbar_arrive_pair(uint32_t bar_cluster)
 {
-    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar_cluster) : "memory");
+    asm volatile("fence.release.sync_restrict::shared::cta.cluster;\n\t"
+                 "mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar_cluster)
+                 : "memory");
 }
 
 // A ring's stage and the parity of its current round, kept running: the single-thread roles are
