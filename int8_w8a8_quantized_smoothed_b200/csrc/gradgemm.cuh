@@ -193,7 +193,8 @@ template <int N> struct Ring {
     }
 };
 
-// mbar_wait for a barrier that the other CTA of the pair arrives on too: acquire at cluster scope.
+// mbar_wait for a barrier that the other CTA of the pair arrives on (the MMAs' commits reach both
+// CTAs): acquire at cluster scope, which costs nothing that could be measured.
 __device__ __forceinline__ bool mbar_wait_cluster(uint32_t bar, uint32_t parity, uint64_t limit_ns)
 {
     uint64_t t0 = 0;
@@ -449,7 +450,7 @@ __global__ void __launch_bounds__(GradCfg<CONV, H>::kThreads, 1)
             const int j0 = jb * kGradTile + static_cast<int>(rank) * 128;
             int r0 = sg.kb0 * kGradBR;
             for (int n = sg.kb1 - sg.kb0; n > 0; --n, ++it, r0 += kGradBR) {
-                if (!mbar_wait(bar_empty + 8 * ring.s, ring.ph ^ 1u, limit_ns)) {
+                if (!mbar_wait_cluster(bar_empty + 8 * ring.s, ring.ph ^ 1u, limit_ns)) {
                     ok = false;
                     break;
                 }
@@ -582,7 +583,7 @@ __global__ void __launch_bounds__(GradCfg<CONV, H>::kThreads, 1)
                 if constexpr (SILU)
                     if (!sg.partial)
                         fetch(0);
-                ok = mbar_wait(bar_tfull + 8 * buf, aph, limit_ns);
+                ok = mbar_wait_cluster(bar_tfull + 8 * buf, aph, limit_ns);
                 if (!ok)
                     break;
                 __syncwarp();
@@ -714,7 +715,7 @@ __global__ void __launch_bounds__(GradCfg<CONV, H>::kThreads, 1)
 #pragma unroll
             for (int k = 0; k < 4; ++k)
                 raw[k] = *reinterpret_cast<const uint4 *>(src + (((2 * k + half + lane) & 7) << 4));
-            if (!mbar_wait(bar_empty + 8 * s, ((it / STAGES) & 1u) ^ 1u, limit_ns))
+            if (!mbar_wait_cluster(bar_empty + 8 * s, ((it / STAGES) & 1u) ^ 1u, limit_ns))
                 break;
             uint8_t *bt = smem + Cfg::kBOff + s * Cfg::kBBytes + row * 128;
 #pragma unroll

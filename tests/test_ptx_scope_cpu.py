@@ -32,6 +32,19 @@ def test_arrivals_on_another_cta_are_at_cluster_scope(path):
             assert ".cluster.shared::cluster" in s, s
 
 
+def test_waits_on_the_pairs_barriers_are_at_cluster_scope():
+    """In the gradient GEMM the even CTA's commits arrive on both CTAs' `empty` and `tfull`, and
+    both CTAs arrive on the even one's `full` and `tempty`: a wait on any of them observes a thread
+    that may be of the other CTA."""
+    with open(os.path.join(build.CSRC, "gradgemm.cuh")) as f:
+        text = f.read()
+    start = text.index("grad_gemm_kernel(const __grid")
+    kernel = text[start:text.index("__global__", start)]
+    waits = re.findall(r"\b(mbar_wait(?:_cluster)?)\(bar_(full|empty|tfull|tempty)\b", kernel)
+    assert {bar for _, bar in waits} == {"full", "empty", "tfull", "tempty"}
+    assert all(fn == "mbar_wait_cluster" for fn, _ in waits), waits
+
+
 def test_the_rule_finds_statements():
     found = [s for p in SOURCES for s in _statements(p) if s.startswith("mbarrier.arrive")]
     assert sum("shared::cluster" in s for s in found) >= 2
