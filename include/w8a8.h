@@ -135,7 +135,8 @@ W8A8_API int w8a8_silu_mul_quant(const w8a8_bf16 *gate_up, int64_t M, int64_t I,
  * workspace must be zero-filled before its first use; every call that returns W8A8_OK
  * leaves it ready for the next one (its flag words zero again), so one buffer serves any
  * number of calls issued in order on one stream. Calls that may run concurrently need
- * separate workspaces.
+ * separate workspaces. A buffer that served a call of "any contents" in between (the gradients,
+ * GPTQ) has to be zero-filled again.
  */
 W8A8_API size_t w8a8_gemm_workspace_size(int64_t M, int64_t N, int64_t K);
 
@@ -359,7 +360,8 @@ W8A8_API int w8a8_sandwich_rmsnorm_quant_fp8(const w8a8_bf16 *y, const w8a8_bf16
  * same bits on the same device. dgamma_post is NULL exactly when gamma_post is, dgate exactly
  * when gate is. dresidual may be dh (in place); no other output may alias an input or another
  * output. Alignment as above (the fp32 gradients need none). workspace:
- * w8a8_sandwich_rmsnorm_backward_workspace_size(M, K) bytes, 16-byte aligned, any contents.
+ * w8a8_sandwich_rmsnorm_backward_workspace_size(M, K) bytes, 16-byte aligned, any contents; it is
+ * left with any contents too (see w8a8_gemm_workspace_size).
  */
 W8A8_API size_t w8a8_sandwich_rmsnorm_backward_workspace_size(int64_t M, int64_t K);
 W8A8_API int w8a8_sandwich_rmsnorm_backward(const w8a8_bf16 *dz, const w8a8_bf16 *dh,
@@ -401,7 +403,8 @@ W8A8_API int w8a8_sandwich_rmsnorm_backward(const w8a8_bf16 *dz, const w8a8_bf16
  * E4M3 NaN codes.
  * Requires M >= 1, N >= 8, N % 8 == 0, K (I) >= 16, K % 16 == 0, each at most 2^30.
  * workspace: w8a8_gemm_dgrad_workspace_size(M, N, K) bytes (dgrad_silu: K = I), or
- * w8a8_gemm_wgrad_workspace_size(M, N, K), 16-byte aligned, any contents (0: may be NULL).
+ * w8a8_gemm_wgrad_workspace_size(M, N, K), 16-byte aligned, any contents (0: may be NULL); it is
+ * left with any contents too (see w8a8_gemm_workspace_size).
  */
 W8A8_API size_t w8a8_gemm_dgrad_workspace_size(int64_t M, int64_t N, int64_t K);
 W8A8_API size_t w8a8_gemm_wgrad_workspace_size(int64_t M, int64_t N, int64_t K);

@@ -219,14 +219,15 @@ def _on_device(fn):
 
 def _scratch(workspace, nbytes, like, index):
     """(address, size, the tensor) of the caller's workspace, or of a new one for this call alone:
-    nothing is kept between calls, so calls on any streams and captured graphs cannot share it."""
+    nothing is kept between calls, so calls on any streams and captured graphs cannot share it. A
+    tensor is left with any contents (to be zeroed before one of the GEMMs gets it)."""
     if workspace is None:
         if nbytes == 0:
             return None, 0, None
         workspace = like.new_empty(nbytes, dtype=torch.uint8)
         return workspace.data_ptr(), nbytes, workspace
     if isinstance(workspace, Workspace):
-        workspace, _ = workspace.get(nbytes)
+        workspace = workspace.scratch(nbytes)
         if workspace is None:
             return None, 0, None
     ptr = _arg(workspace, "workspace", workspace.dtype, None, index)
@@ -425,13 +426,16 @@ def w8a8_gemm_workspace_size_ex(M, N, K, variant=0, ctas=0, tile_n=0) -> int:
 
 
 class Workspace:
-    """A zero-filled device workspace that grows on demand (the library never allocates).
-    One instance serves calls issued in order on one stream."""
+    """A device workspace that grows on demand (the library never allocates). One instance serves
+    calls of every kind issued in order on one stream: it keeps a zero-filled buffer for the GEMMs,
+    which leave its flag words zero, and another for the calls that leave any contents behind (the
+    gradients)."""
 
     def __init__(self, device=None):
         self.device = torch.device("cuda", torch.cuda.current_device()) if device is None \
             else torch.device(device)
         self.buf = None
+        self.scratch_bufs = []
 
     def get(self, nbytes):
         if nbytes == 0:
@@ -439,6 +443,17 @@ class Workspace:
         if self.buf is None or self.buf.numel() < nbytes:
             self.buf = torch.zeros(max(nbytes, 1 << 20), dtype=torch.uint8, device=self.device)
         return self.buf, self.buf.numel()
+
+    def scratch(self, nbytes):
+        """A buffer of any contents, never the zero-filled one. It at least doubles when it grows,
+        and the outgrown ones are kept: a captured graph may still use them."""
+        if nbytes == 0:
+            return None
+        have = self.scratch_bufs[-1].numel() if self.scratch_bufs else 0
+        if have < nbytes:
+            self.scratch_bufs.append(torch.empty(max(nbytes, 2 * have), dtype=torch.uint8,
+                                                 device=self.device))
+        return self.scratch_bufs[-1]
 
 
 _default_ws = {}
