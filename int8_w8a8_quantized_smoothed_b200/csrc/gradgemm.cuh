@@ -574,7 +574,7 @@ __global__ void __launch_bounds__(GradCfg<CONV, H>::kThreads, 1)
                 auto fetch = [&](int c) {
                     const int j0 = jb * kGradTile + c * 32;
                     const char *gu = reinterpret_cast<const char *>(gate_up) + row0 * ld + j0 * 2;
-                    const int bytes = min(64, (w.J - j0) * 2);
+                    const int bytes = 2 * min(32, w.J - j0);
                     uint4 *to = stage_w + (c & 1) * 256;
                     stage_load<4>(to, lane, gu, ld, rows, bytes);
                     stage_load<4>(to + 128, lane, gu + static_cast<int64_t>(w.J) * 2, ld, rows, bytes);
@@ -625,7 +625,7 @@ __global__ void __launch_bounds__(GradCfg<CONV, H>::kThreads, 1)
                         }
                         __syncwarp();
                         char *dst = reinterpret_cast<char *>(out) + row0 * ld + j0 * 2;
-                        const int bytes = min(64, (w.J - j0) * 2);
+                        const int bytes = 2 * min(32, w.J - j0);
                         stage_store<4>(st, lane, dst, ld, rows, bytes);
                         stage_store<4>(st + 128, lane, dst + static_cast<int64_t>(w.J) * 2, ld, rows,
                                        bytes);
@@ -643,7 +643,7 @@ __global__ void __launch_bounds__(GradCfg<CONV, H>::kThreads, 1)
                             __syncwarp();
                             stage_store<8>(stage_w, lane,
                                            reinterpret_cast<char *>(out) + row0 * ld + (j0 - 32) * 2, ld,
-                                           rows, min(128, (w.J - j0 + 32) * 2));
+                                           rows, 2 * min(64, w.J - j0 + 32)); // J up to 2^30
                         }
                     }
                     __syncwarp();
