@@ -316,8 +316,8 @@ W8A8_API int w8a8_gemm_rmsnorm_quant_ex(const int8_t *xq, const float *s_tok, co
  *   z[m,j]  = (h[m,j] * r2[m]) * gamma_smoothed[j]
  *   s_tok, q from z exactly as in w8a8_quantize_rows (_fp8: w8a8_quantize_rows_fp8)
  * with r1 = 1 / sqrt(mean(y^2) + eps_post), r2 = 1 / sqrt(mean(h^2) + eps), the means summed in
- * binary64 or as binary32 pairs (within 2^-44) and rounded once, and every other product and sum
- * its own binary32 operation. gate_kind says what `gate` is: W8A8_GATE_NONE (gate NULL), W8A8_GATE_TOKEN (fp32
+ * binary64 or as binary32 pairs (within 2^-38) and rounded once to binary32 (so they have to be
+ * below 2^128), and every other product and sum its own binary32 operation. gate_kind says what `gate` is: W8A8_GATE_NONE (gate NULL), W8A8_GATE_TOKEN (fp32
  * [M], one factor per token), W8A8_GATE_CHANNEL (fp32 [K]), W8A8_GATE_FULL (bf16 [M,K]).
  * y, residual, h_out: bf16 [M,K]; gamma_post, gamma_smoothed: fp32 [K]; q [M,K]; s_tok fp32 [M];
  * all but s_tok and a per-token gate 16-byte aligned. h_out may be residual (in place), nothing

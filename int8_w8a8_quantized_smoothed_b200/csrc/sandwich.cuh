@@ -173,8 +173,11 @@ template <int W> __device__ __forceinline__ void team_sync(int team)
 }
 
 // Running sum of squares of values that are exact in bf16 (so are their squares in binary32): a
-// binary32 sum and the sum of its additions' exact errors, two lanes at a time. The two carry
-// about 2^-46 of the sum, with a fraction of the time of binary64 conversions and additions.
+// binary32 sum and the sum of its additions' exact errors, two lanes at a time, with a fraction of
+// the time of binary64 conversions and additions. With u = 2^-24 and at most 32 values in a sum S,
+// an addition's error is at most u S and the sum of i of them at most i u S, so rounding those sums
+// costs at most (1 + .. + 32) u^2 S < 2^-38 S (2^-46 in practice). Where the binary32 sum
+// overflows, value() is infinite or NaN, and the row is summed again in binary64.
 struct SquareSum {
     float2 hi = make_float2(0.0f, 0.0f), lo = make_float2(0.0f, 0.0f);
     __device__ __forceinline__ void add(float2 a)
@@ -207,6 +210,24 @@ __device__ __forceinline__ double team_sum(double v, double *sh, int team, int w
             v = __dadd_rn(v, sh[w]);
     }
     return v;
+}
+
+// The sum of squares of a team's row again, in binary64 as the kernel above has it; value(c, v)
+// gives the thread's vector c.
+template <int W, typename Value>
+__device__ __forceinline__ double team_resum(Value value, int nvec, int tl, double *sh, int team,
+                                             int warp_in_team, int lane)
+{
+    double t = 0.0;
+#pragma unroll 1
+    for (int c = 0; c < kTeamVecs; ++c)
+        if (c * 32 * W + tl < nvec) {
+            float v[1][8];
+            value(c, v[0]);
+            t = __dadd_rn(t, square_sum<1>(v));
+        }
+    team_sync<W>(team); // all have read the first sums
+    return team_sum<W>(t, sh, team, warp_in_team, lane);
 }
 
 template <int W, bool POST, int GATE, bool F8>
@@ -282,7 +303,10 @@ __global__ void __launch_bounds__(512, 1) sandwich_rows_kernel(const SandwichRow
                         ss.add(make_float2(v[c][i], v[c][i + 1]));
                 }
             }
+            auto y = [&](int c, float (&x)[8]) { unpack8(mine[c * 32 * W + tl], x); };
             r1 = rstd_of(team_sum<W>(ss.value(), sums, team, wt, lane), a.K, a.eps_post);
+            if (!(r1 > 0.0f)) // the sum has overflowed, for the whole team alike
+                r1 = rstd_of(team_resum<W>(y, nvec, tl, sums, team, wt, lane), a.K, a.eps_post);
         }
         float gt = 1.0f;
         if constexpr (GATE == kGateToken)
@@ -325,10 +349,17 @@ __global__ void __launch_bounds__(512, 1) sandwich_rows_kernel(const SandwichRow
                     ss.add(make_float2(v[c][i], v[c][i + 1]));
             }
         }
-        const float r2 = rstd_of(team_sum<W>(ss.value(), sums + 4, team, wt, lane), a.K, a.eps_pre);
+        const double hh = team_sum<W>(ss.value(), sums + 4, team, wt, lane);
         // the whole team has used what it read of this row: its place is free
         if (tl == 0 && row + stride < a.M)
             fetch(row + stride);
+        float r2 = rstd_of(hh, a.K, a.eps_pre);
+        if (!(r2 > 0.0f)) { // as r1; h comes from where this thread has just stored it
+            auto h = [&](int c, float (&x)[8]) {
+                unpack8(reinterpret_cast<const uint4 *>(a.h)[row * nvec + c * 32 * W + tl], x);
+            };
+            r2 = rstd_of(team_resum<W>(h, nvec, tl, sums + 4, team, wt, lane), a.K, a.eps_pre);
+        }
         float amax = 0.0f;
 #pragma unroll
         for (int c = 0; c < kTeamVecs; ++c) {
