@@ -356,8 +356,9 @@ W8A8_API int w8a8_sandwich_rmsnorm_quant_fp8(const w8a8_bf16 *y, const w8a8_bf16
  *   dgamma_smoothed[j] = sum_m dz h r2;  dgamma_post[j] = sum_m gate D y r1
  *   dgate        = D n: summed over the channels (W8A8_GATE_TOKEN, fp32 [M]), over the tokens
  *                  (W8A8_GATE_CHANNEL, fp32 [K]), or elementwise (W8A8_GATE_FULL, bf16 [M,K])
- * The sums over tokens are taken per CTA and then added in a fixed order: the same call gives the
- * same bits on the same device. dgamma_post is NULL exactly when gamma_post is, dgate exactly
+ * The row sums (h h, y y, w h, and those of y's terms with dh, w and h) are binary32 and have to
+ * stay below 2^128. The sums over tokens are taken per CTA and then added in a fixed order: the same
+ * call gives the same bits on the same device. dgamma_post is NULL exactly when gamma_post is, dgate exactly
  * when gate is. dresidual may be dh (in place); no other output may alias an input or another
  * output. Alignment as above (the fp32 gradients need none). workspace:
  * w8a8_sandwich_rmsnorm_backward_workspace_size(M, K) bytes, 16-byte aligned, any contents; it is

@@ -638,10 +638,12 @@ __global__ void __launch_bounds__(kBackMaxThreads, 1) sandwich_back_kernel(const
         if constexpr (GATE == kGateToken)
             gt = a.gate ? __ldg(static_cast<const float *>(a.gate) + row) : 1.0f;
         const float r2 = 1.0f / sqrtf(fmaf(t[0], invK, a.eps_pre));
-        const float c2 = r2 * r2 * r2 * (t[1] * invK);
+        // r2^3 A / K and r1^3 S / K without one factor, which goes to h and to y: 1 / rms may be large
+        // enough (from 2^43 on) for its cube to overflow
+        const float c2 = t[1] * invK * r2 * r2;
         const float r1 = POST ? 1.0f / sqrtf(fmaf(t[2], invK, a.eps_post)) : 1.0f;
-        const float sp = fmaf(-c2, t[5], fmaf(r2, t[4], t[3])); // sum p D
-        const float c1 = r1 * r1 * r1 * (gt * sp * invK);
+        const float sp = fmaf(-c2, r2 * t[5], fmaf(r2, t[4], t[3])); // sum p D
+        const float c1 = gt * sp * invK * r1 * r1;
         if constexpr (GATE == kGateToken)
             if (a.dgate_tok && threadIdx.x == 0 && rank == 0)
                 a.dgate_tok[row] = r1 * sp;
@@ -662,10 +664,10 @@ __global__ void __launch_bounds__(kBackMaxThreads, 1) sandwich_back_kernel(const
 #pragma unroll
                     for (int c = 0; c < 2; ++c) {
                         const int i = 4 * hv + 2 * e + c;
-                        const float hh = c ? h2.y : h2.x, x1 = (c ? y2.y : y2.x) * r1;
+                        const float x2 = (c ? h2.y : h2.x) * r2, x1 = (c ? y2.y : y2.x) * r1;
                         const float zz = c ? dz2.y : dz2.x;
-                        const float D = fmaf(r2, zz * gp[i], fmaf(-c2, hh, c ? dh2.y : dh2.x));
-                        acc_pre[i] = fmaf(zz * r2, hh, acc_pre[i]);
+                        const float D = fmaf(r2, zz * gp[i], fmaf(-c2, x2, c ? dh2.y : dh2.x));
+                        acc_pre[i] = fmaf(zz, x2, acc_pre[i]);
                         od[c] = D * a.res_scale;
                         // a gate that varies along the row is in gq (per channel) or in g
                         const float gd = GATE == kGateToken ? gt * D
@@ -674,7 +676,7 @@ __global__ void __launch_bounds__(kBackMaxThreads, 1) sandwich_back_kernel(const
                             acc_t[i] = fmaf(gd, x1, acc_t[i]);
                         if constexpr (GATE == kGateFull)
                             og[c] = D * (x1 * gq[i]);
-                        oy[c] = POST ? fmaf(r1 * gq[i], gd, -c1 * (c ? y2.y : y2.x)) : gq[i] * gd;
+                        oy[c] = POST ? fmaf(r1 * gq[i], gd, -c1 * x1) : gq[i] * gd;
                     }
                     ores[2 * hv + e] = pack_bf16x2(od[0], od[1]);
                     ody[2 * hv + e] = pack_bf16x2(oy[0], oy[1]);
