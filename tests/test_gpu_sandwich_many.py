@@ -65,3 +65,114 @@ def test_backward_of_small_rows_without_eps(scale, post, kind):
         _check("dgamma_post", host(got[3]), *ref["dgamma_post"], n + M + 136, False)
     if kind == "token":
         _check("dgate", host(got[4]), *ref["dgate"], n + M + 136, False)
+
+
+def _rows(M, K, seed, std=1.0):
+    """bf16 [M, K] on the device, one channel in a hundred fifty times as wide."""
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    x = torch.randn(M, K, generator=g, device="cuda") * std
+    wide = torch.rand(K, generator=g, device="cuda") < 0.01
+    return (x * torch.where(wide, 50.0, 1.0)).bfloat16()
+
+
+def _gate_on_device(kind, M, K, seed):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    shape = {"none": None, "token": (M, 1), "channel": (1, K), "full": (M, K)}[kind]
+    if shape is None:
+        return None
+    x = torch.randn(shape, generator=g, device="cuda")
+    return x.bfloat16() if kind == "full" else x
+
+
+def _gain(K, seed):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    return 1 + 0.1 * torch.randn(K, generator=g, device="cuda")
+
+
+def _replayed(call, want, before=lambda: None):
+    """Six calls of a graph, replayed three times, each with the first call's bits."""
+    g = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(g):
+        outs = [call(i) for i in range(6)]
+    for _ in range(3):
+        before()
+        g.replay()
+        for o in outs:
+            for a, b in zip(o, want):
+                assert b is None or torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+    assert w8.w8a8_last_device_status() == 0
+
+
+KINDS = [("none", False, False), ("none", True, True), ("token", True, False),
+         ("channel", False, True), ("channel", True, False), ("full", True, True),
+         ("full", False, False)]
+
+
+# one, two and four warps a row, with up to sixteen, eight and four rows of an SM at a time, three
+# rows and more each; then one row a CTA with more rows than resident CTAs (narrow rows of few
+# values in all; rows of more than 8192)
+@pytest.mark.parametrize("M,K", [(8003, 208), (2501, 2064), (1301, 4112), (1301, 8192),
+                                 (20011, 64), (5501, 272), (761, 2064), (601, 14336),
+                                 (301, 32768)])
+@pytest.mark.parametrize("kind,post,f8", KINDS)
+def test_forward_row_after_row(M, K, kind, post, f8):
+    y, res, gs = _rows(M, K, 51), _rows(M, K, 52), _gain(K, 53)
+    gp = _gain(K, 54) if post else None
+    gate = _gate_on_device(kind, M, K, 55)
+    fn = w8.w8a8_sandwich_rmsnorm_quant_fp8 if f8 else w8.w8a8_sandwich_rmsnorm_quant
+
+    def call(r, **kw):
+        return fn(y, r, gs, EPS, gamma_post=gp, eps_post=EPS_POST, gate=gate, res_scale=0.75, **kw)
+
+    q, s, h = call(res)
+    # against the oracle on some of the rows, the first and the last among them
+    some = np.unique(np.r_[0, M - 1, np.random.default_rng(M).integers(0, M, 96)])
+    at = torch.from_numpy(some).cuda()
+    hg = None
+    if gate is not None:
+        hg = gate if kind == "channel" else gate[at]
+        hg = host(hg.float())
+    ref_h = _h_reference(_f(host_bf16(y[at])), _f(host_bf16(res[at])),
+                         None if gp is None else host(gp), hg, 0.75)
+    assert np.array_equal(host_bf16(h[at]), ref_h)
+    assert_rms_rows_match(host(q.view(torch.uint8)[at] if f8 else q[at]), host(s[at]), ref_h,
+                          host(gs), EPS, ref_fn=oracle.smooth_rmsnorm_quant_fp8 if f8 else
+                          oracle.smooth_rmsnorm_quant)
+    # one call right after another, each in place on a residual of its own: all rows, bit for bit
+    places = [res.clone() for _ in range(6)]
+    _replayed(lambda i: call(places[i], h_out=places[i]), (q, s, h),
+              lambda: [p.copy_(res) for p in places])
+
+
+# clusters of two, three and four CTAs (the last one with fewer columns), and one CTA: three rows
+# and more each
+@pytest.mark.parametrize("M,K", [(250, 8208), (160, 16400), (120, 24592), (1500, 1040)])
+@pytest.mark.parametrize("kind,post,with_dh", KINDS)
+def test_backward_row_after_row(M, K, kind, post, with_dh):
+    y, h, gs = _rows(M, K, 61), _rows(M, K, 62), _gain(K, 63)
+    gp = _gain(K, 64) if post else None
+    gate = _gate_on_device(kind, M, K, 65)
+    dz = _rows(M, K, 66, 0.01)
+    dh = _rows(M, K, 67, 0.01) if with_dh else None
+
+    def call(_):
+        return w8.w8a8_sandwich_rmsnorm_backward(dz, y, h, gs, EPS, dh=dh, gamma_post=gp,
+                                                 eps_post=EPS_POST, gate=gate, res_scale=0.75)
+
+    got = call(0)
+    d = lambda t: None if t is None else host(t.double())  # noqa: E731
+    ref = backward(d(dz), d(y), d(h), d(gs), EPS, dh=d(dh), gamma_post=d(gp), eps_post=EPS_POST,
+                   gate=d(gate), res_scale=0.75)
+    # a row sum adds 8 values in a thread, then over 32 lanes, up to 32 warps and 4 CTAs (8 + 5 + 5
+    # + 4 additions), twice in a row for dy, with the factors around them: below 128; a sum over the
+    # tokens adds at most one for each of a CTA's rows and each part of a lane: below M, and 136
+    n, tokens = 128, 128 + M + 136
+    _check("dy", d(got[0]), *ref["dy"], n, True)
+    _check("dresidual", d(got[1]), *ref["dresidual"], n, True)
+    _check("dgamma_pre", host(got[2]), *ref["dgamma_pre"], tokens, False)
+    if post:
+        _check("dgamma_post", host(got[3]), *ref["dgamma_post"], tokens, False)
+    if kind != "none":
+        _check("dgate", d(got[4]), *ref["dgate"], n if kind == "full" else tokens, kind == "full")
+    _replayed(call, got)
