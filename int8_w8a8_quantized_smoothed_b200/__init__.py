@@ -196,13 +196,18 @@ def _matrix(t, name, dtype):
 
 
 def _on_device(fn):
-    """Runs a call with its first tensor's device current and on the given stream (default: that
-    device's current stream), so that outputs and workspaces allocated inside belong to the stream
-    that uses them."""
-    first = next(iter(inspect.signature(fn).parameters))
+    """Runs a call with its first tensor's device current and on the given stream (the function's
+    last parameter; default: that device's current stream), so that outputs and workspaces allocated
+    inside belong to the stream that uses them."""
+    first, *_, last = names = list(inspect.signature(fn).parameters)
+    assert last == "stream"
 
     @functools.wraps(fn)
     def call(*args, stream=None, **kw):
+        if len(args) == len(names):
+            if stream is not None:
+                raise TypeError(f"{fn.__name__}() got multiple values for argument 'stream'")
+            *args, stream = args
         x = args[0] if args else kw.get(first)
         if not isinstance(x, torch.Tensor) or not x.is_cuda:
             return fn(*args, **kw)  # which says what is wrong with it
@@ -841,12 +846,13 @@ def _sandwich_quant(name, code, y, residual, gamma_smoothed, eps, gamma_post, ep
 
 @_on_device
 def w8a8_sandwich_rmsnorm_quant(y, residual, gamma_smoothed, eps, gamma_post=None, eps_post=None,
-                                gate=None, res_scale=1.0, h_out=None, q=None, s_tok=None):
+                                gate=None, res_scale=1.0, h_out=None, q=None, s_tok=None,
+                                stream=None):
     """The step between two blocks: h = bf16(res_scale * residual + gate * n), with n the RMSNorm
     of the block's output y by gamma_post (n = y without gamma_post), then the next block's
     smoothed RMSNorm of h with per-token int8 codes. gate: None, fp32 [M, 1] (per token), fp32
     [1, K] (per channel) or bf16 [M, K]. eps_post defaults to eps. h_out may be residual (in
-    place). stream: by keyword, default the current one. Returns (q, s_tok, h)."""
+    place). stream: default the current one. Returns (q, s_tok, h)."""
     return _sandwich_quant("w8a8_sandwich_rmsnorm_quant", torch.int8, y, residual, gamma_smoothed,
                            eps, gamma_post, eps_post, gate, res_scale, h_out, q, s_tok)
 
@@ -854,7 +860,7 @@ def w8a8_sandwich_rmsnorm_quant(y, residual, gamma_smoothed, eps, gamma_post=Non
 @_on_device
 def w8a8_sandwich_rmsnorm_quant_fp8(y, residual, gamma_smoothed, eps, gamma_post=None,
                                     eps_post=None, gate=None, res_scale=1.0, h_out=None, q=None,
-                                    s_tok=None):
+                                    s_tok=None, stream=None):
     """w8a8_sandwich_rmsnorm_quant with FP8 (E4M3) codes."""
     return _sandwich_quant("w8a8_sandwich_rmsnorm_quant_fp8", FP8, y, residual, gamma_smoothed,
                            eps, gamma_post, eps_post, gate, res_scale, h_out, q, s_tok)
@@ -867,11 +873,11 @@ def w8a8_sandwich_rmsnorm_backward_workspace_size(M: int, K: int) -> int:
 @_on_device
 def w8a8_sandwich_rmsnorm_backward(dz, y, h, gamma_smoothed, eps, dh=None, gamma_post=None,
                                    eps_post=None, gate=None, res_scale=1.0, dy=None,
-                                   dresidual=None, workspace=None):
+                                   dresidual=None, workspace=None, stream=None):
     """The backward pass of w8a8_sandwich_rmsnorm_quant (either code), the quantization passed
     straight through: dz bf16 [M, K] is the gradient of the codes' values, dh bf16 [M, K] (or
     None) the gradient that reaches h by the residual stream, y and h the forward call's input
-    and stored output. dresidual may be dh (in place). stream: by keyword, default the current
+    and stored output. dresidual may be dh (in place). stream: default the current
     one. Returns (dy, dresidual, dgamma_smoothed, dgamma_post or None, dgate or None), dgate in
     gate's shape and type."""
     M, K, index = _matrix(dz, "dz", torch.bfloat16)
@@ -940,23 +946,23 @@ def _grad(name, code, dy, q, scale, rows, out, out_name, gate_up, workspace):
 
 
 @_on_device
-def w8a8_gemm_dgrad(dy, wq, s_ch, dx=None, workspace=None):
+def w8a8_gemm_dgrad(dy, wq, s_ch, dx=None, workspace=None, stream=None):
     """Input gradient of a W8A8 linear: dx [M, K] = dy [M, N] @ (wq * s_ch[:, None]) in bf16, the
-    weight's int8 codes dequantized by the library. stream: by keyword, default the current one."""
+    weight's int8 codes dequantized by the library. stream: default the current one."""
     return _grad("w8a8_gemm_dgrad", torch.int8, dy, wq, s_ch, 1, dx, "dx", None, workspace)
 
 
 @_on_device
-def w8a8_gemm_dgrad_fp8(dy, wq, s_ch, dx=None, workspace=None):
+def w8a8_gemm_dgrad_fp8(dy, wq, s_ch, dx=None, workspace=None, stream=None):
     """w8a8_gemm_dgrad with FP8 (E4M3) weight codes."""
     return _grad("w8a8_gemm_dgrad_fp8", FP8, dy, wq, s_ch, 1, dx, "dx", None, workspace)
 
 
 @_on_device
-def w8a8_gemm_dgrad_silu(dy, wq, s_ch, gate_up, dgate_up=None, workspace=None):
+def w8a8_gemm_dgrad_silu(dy, wq, s_ch, gate_up, dgate_up=None, workspace=None, stream=None):
     """The gated feed-forward block's backward step: da = dy [M, H] @ (wq * s_ch[:, None]) with the
     down projection's wq [H, I], then the gradients of silu(gate) * up from the forward gate|up
-    values gate_up [M, 2I]. stream: by keyword, default the current one. Returns dgate_up [M, 2I];
+    values gate_up [M, 2I]. stream: default the current one. Returns dgate_up [M, 2I];
     da is not stored."""
     if gate_up is None:
         raise TypeError("gate_up must be a torch.Tensor")
@@ -965,7 +971,7 @@ def w8a8_gemm_dgrad_silu(dy, wq, s_ch, gate_up, dgate_up=None, workspace=None):
 
 
 @_on_device
-def w8a8_gemm_dgrad_silu_fp8(dy, wq, s_ch, gate_up, dgate_up=None, workspace=None):
+def w8a8_gemm_dgrad_silu_fp8(dy, wq, s_ch, gate_up, dgate_up=None, workspace=None, stream=None):
     """w8a8_gemm_dgrad_silu with FP8 (E4M3) weight codes."""
     if gate_up is None:
         raise TypeError("gate_up must be a torch.Tensor")
@@ -974,14 +980,14 @@ def w8a8_gemm_dgrad_silu_fp8(dy, wq, s_ch, gate_up, dgate_up=None, workspace=Non
 
 
 @_on_device
-def w8a8_gemm_wgrad(dy, xq, s_tok, dw=None, workspace=None):
+def w8a8_gemm_wgrad(dy, xq, s_tok, dw=None, workspace=None, stream=None):
     """Weight gradient of a W8A8 linear, passed straight through the weight's rounding: dw [N, K] =
     dy [M, N]^T @ (xq * s_tok[:, None]) in bf16, the activations' int8 codes dequantized by the
-    library. stream: by keyword, default the current one."""
+    library. stream: default the current one."""
     return _grad("w8a8_gemm_wgrad", torch.int8, dy, xq, s_tok, 0, dw, "dw", None, workspace)
 
 
 @_on_device
-def w8a8_gemm_wgrad_fp8(dy, xq, s_tok, dw=None, workspace=None):
+def w8a8_gemm_wgrad_fp8(dy, xq, s_tok, dw=None, workspace=None, stream=None):
     """w8a8_gemm_wgrad with FP8 (E4M3) activation codes."""
     return _grad("w8a8_gemm_wgrad_fp8", FP8, dy, xq, s_tok, 0, dw, "dw", None, workspace)

@@ -60,3 +60,17 @@ def test_one_workspace_serves_forward_and_gradient_calls():
         for got, want in zip(_forward(t, ws), want_f):
             assert torch.equal(got, want)
     assert w8.w8a8_last_device_status() == 0
+
+
+def test_stream_by_position():
+    t = _inputs()
+    want = w8.w8a8_gemm_dgrad(t["dy"], t["w"], t["sc"])
+    wq, ws, wh = w8.w8a8_sandwich_rmsnorm_quant(t["dy"], t["res"], t["gamma"], 1e-5)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    got = w8.w8a8_gemm_dgrad(t["dy"], t["w"], t["sc"], None, None, side)
+    q, s, h = w8.w8a8_sandwich_rmsnorm_quant(t["dy"], t["res"], t["gamma"], 1e-5, None, None, None,
+                                             1.0, None, None, None, side)
+    side.synchronize()
+    assert torch.equal(got, want) and torch.equal(q, wq) and torch.equal(h, wh)
+    assert torch.equal(s, ws)
