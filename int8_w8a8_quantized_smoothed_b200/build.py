@@ -68,9 +68,15 @@ def build(force: bool = False, verbose: bool = False) -> str:
         cmd = [nvcc(), *NVCC_FLAGS, "-I", os.path.join(ROOT, "include"), "-I", CSRC]
         if verbose:
             cmd += ["-Xptxas", "-v"]
-        cmd += ["-c", src, "-o", obj]
-        jobs.append((cmd, subprocess.Popen(cmd)))
-    failed = [cmd for cmd, p in jobs if p.wait() != 0]
+        # an object takes its place only when it is whole: one cut short would count as built
+        cmd += ["-c", src, "-o", f"{obj}.{os.getpid()}.tmp.o"]
+        jobs.append((cmd, obj, subprocess.Popen(cmd)))
+    failed = []
+    for cmd, obj, p in jobs:
+        if p.wait() != 0:
+            failed.append(cmd)
+        else:
+            os.replace(cmd[-1], obj)
     if failed:
         raise subprocess.CalledProcessError(1, failed[0])
     subprocess.run([nvcc(), *LINK_FLAGS, *objs, "-o", LIB + ".tmp"], check=True)
