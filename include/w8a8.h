@@ -396,7 +396,8 @@ W8A8_API int w8a8_sandwich_rmsnorm_backward(const w8a8_bf16 *dz, const w8a8_bf16
  * dy: bf16 [M,N], the gradient of the linear's output (N of the down projection: the hidden
  * size). wq [N,K] and s_ch fp32 [N]: the forward call's weight; xq [M,K] and s_tok fp32 [M]: its
  * activations; codes as int8, or E4M3 as uint8 (_fp8). gate_up: bf16 [M,2I], the forward gate|up
- * output ([gate | up] halves, as w8a8_silu_mul_quant reads it); dgate_up likewise. For the gate|up
+ * output ([gate | up] halves, as w8a8_silu_mul_quant reads it; w8a8_gemm_silu_quant does not store
+ * it, so the forward pass is w8a8_gemm_dequant, then w8a8_silu_mul_quant); dgate_up likewise. For the gate|up
  * projection itself the rows of wq and the columns of dy only have to agree, so the interleaved
  * weight of w8a8_gemm_silu_quant serves with dy interleaved alike. dx: bf16 [M,K]; dw: bf16 [N,K].
  * Every matrix 16-byte aligned; no output may alias an input. Scales finite and at least

@@ -962,8 +962,8 @@ def w8a8_gemm_dgrad_fp8(dy, wq, s_ch, dx=None, workspace=None, stream=None):
 def w8a8_gemm_dgrad_silu(dy, wq, s_ch, gate_up, dgate_up=None, workspace=None, stream=None):
     """The gated feed-forward block's backward step: da = dy [M, H] @ (wq * s_ch[:, None]) with the
     down projection's wq [H, I], then the gradients of silu(gate) * up from the forward gate|up
-    values gate_up [M, 2I]. stream: default the current one. Returns dgate_up [M, 2I];
-    da is not stored."""
+    values gate_up [M, 2I] (of w8a8_gemm_dequant; the fused w8a8_gemm_silu_quant does not store
+    them). stream: default the current one. Returns dgate_up [M, 2I]; da is not stored."""
     if gate_up is None:
         raise TypeError("gate_up must be a torch.Tensor")
     return _grad("w8a8_gemm_dgrad_silu", torch.int8, dy, wq, s_ch, 1, dgate_up, "dgate_up",

@@ -277,20 +277,22 @@ constexpr int64_t kGradNarrowRows = 128;
 // ahead of the product: a pass over Q of 3 bytes a code, after which the GEMM is free of the
 // conversions that the other form makes again for every 512 rows, and of that form's tile ends with
 // nothing to hide behind. With longer sums the two take the same time and the pass would only cost
-// its workspace (us, converting in the kernel / ahead: 4096 x 2048 x 4096 62 / 54, 8192 x 4096 x
-// 4096 218 / 186, 4096 x 8192 x 4096 207 / 208, 4096 x 28672 x 4096 sustained 804 / 820;
-// 2048 x 28672 x 4096 349 / 425).
+// its workspace (us, converting in the kernel / ahead: 4096 x 2048 x 4096 60 / 54, 8192 x 4096 x
+// 4096 212 / 188, 4096 x 8192 x 4096 208 / 204, 4096 x 28672 x 4096 703 / 707;
+// 2048 x 28672 x 4096 351 / 396).
 constexpr int64_t kGradDequantRows = 4096, kGradDequantSum = 8192;
 // The kernel that converts Q itself has tiles of 256 x 256, or of 512 x 256 with half the
 // conversions but nothing to hide a tile's end behind: a k-block of either, and that end, us. (By
-// 512 x 256 / 256 x 256: 2048 x 28672 x 4096 349 / 390 us, 2048 x 4096 x 4096 55 / 61, sustained
-// 394 / 447 and 55 / 62; wgrad 1024 x 4000 x 4096 38 / 35, silu 512 x 4096 x 14336 77 / 74. Of 45
-// random shapes the plan came within 5% of the better height in 43, within 6% in all.)
+// 512 x 256 / 256 x 256: 2048 x 28672 x 4096 351 / 401 us, 2048 x 4096 x 4096 59 / 63, 512 x 4096 x
+// 14336 with the SiLU epilogue 77 / 75, wgrad 1024 x 4000 x 4096 39 / 36. Of 45 random shapes the
+// plan came within 5% of the better height in 43, within 6% in all.)
 constexpr double kConvOneUs = 0.46, kConvTwoUs = 0.79, kTailUs = 5.0, kTailSiluUs = 8.0;
 // Operands of up to this many bytes stay in L2 (126 MB) from one use to the next.
 constexpr int64_t kGradL2Bytes = 64 << 20;
 
-// The tiles of one form and how many pairs (CTAs) share the last ones; returns the time, us.
+// The tiles of one form and how many pairs (CTAs) share the last ones; returns an estimate, us, for
+// comparing plans. It is not the time: it leaves out a launch's start, and counts no end of the
+// 256-row tiles (512 x 4096 x 14336 with the SiLU epilogue: 57, measured 75).
 // The last tiles' k-blocks are split over more pairs where that saves more than the partial tiles
 // cost: a k-block takes `each` us and a tile's end `tail` us more, the second launch about 3 us, and
 // the partial tiles are stored and read at about 6 MB a us.

@@ -8,7 +8,10 @@
 //
 // Both sum over the rows of the 8-bit matrix Q, which is the dimension its scales belong to, so
 // the scale cannot wait for the epilogue: Q becomes a scaled bf16 operand, its codes exact in bf16
-// and the product with the scale rounded once. Three forms:
+// and the product with the scale rounded once. That rounding, the same as a weight dequantized to
+// bf16 has, is as large as the output's: with the two the 2-norm error is 2.3e-3 of the result's,
+// with the output's alone 1.7e-3. Without it (dy s in two bf16 parts against the bare codes) there
+// would be twice the MMAs, which set the time of all but the narrow form. Three forms:
 //   narrow    at most 128 rows i of an input gradient: the codes are streamed once, converted into
 //             tensor memory (below);
 //   CONV      warps of the kernel turn Q's tiles into bf16 tiles in shared memory: a code is read
@@ -32,7 +35,7 @@ constexpr int kGradBR = 64;    // r per k-block: one 128-byte row of bf16
 // evenly over rem_pairs pairs, whose partial tiles grad_fixup_kernel adds.
 struct GradWork {
     int I, J, R;
-    int tile_i, tile_j; // 256 x 256 for a CTA pair; narrow kernel: 16 .. 128 x 128 for a CTA
+    int tile_i, tile_j; // 256 or 512 x 256 for a CTA pair; narrow kernel: 16 .. 128 x 128 for a CTA
     int ni, nj, kblocks, group_i;
     int npairs, whole, rem, rem_pairs; // (narrow kernel: CTAs)
 };
@@ -170,8 +173,8 @@ __device__ __forceinline__ uint64_t sw128_mnmajor_desc(uint32_t saddr)
 // the odd CTA's stores are published to a thread outside it, but of stores to this CTA's shared
 // memory alone (each behind its own thread's proxy fence): a release of all of memory took about
 // 2000 cycles, which four groups of converters could not hide (2048 x 28672 x 4096 in tiles of 256
-// rows 440 us against 390), nor could a warp that passes the groups' arrivals on (in tiles of 512
-// rows 396 us; 349 with a release at CTA scope, too narrow, 342 with this one).
+// rows 440 us, 401 with this one), nor could a warp that passes the groups' arrivals on (in tiles of
+// 512 rows 396 us, 343 to 351 with this one).
 __device__ __forceinline__ void mbar_arrive_pair(uint32_t bar_cluster)
 {
     asm volatile("fence.release.sync_restrict::shared::cta.cluster;\n\t"
@@ -374,8 +377,8 @@ __device__ __forceinline__ void stage_store(const uint4 *stage, int lane, char *
 // A CTA pair per 256 H x 256 tile (cta_group::2): each CTA holds 128 rows of A a half and 128
 // columns of B and accumulates 128 x 256 a half. WGRAD: A is MN-major. SILU: the epilogue turns
 // C = da into dg and du (out is [I, 2J]) with the forward call's gate|up values.
-// Bound by the power limit in long runs: 2048 x 28672 x 4096 takes 349 us = 1.38 PFLOP/s, sustained
-// 394 us at 1.57 GHz (the bare bf16 product by a library 316 and 351 us); a k-block of 512 rows
+// Bound by the power limit in long runs: 2048 x 28672 x 4096 takes 347 us = 1.39 PFLOP/s, sustained
+// 398 us at 1.57 GHz (the bare bf16 product by a library 316 and 351 us); a k-block of 512 rows
 // takes about 1250 cycles, of them 1024 of MMA.
 template <bool CONV, int H, bool WGRAD, bool F8, bool SILU>
 __global__ void __launch_bounds__(GradCfg<CONV, H>::kThreads, 1)
