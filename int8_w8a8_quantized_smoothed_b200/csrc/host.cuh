@@ -73,6 +73,19 @@ inline int current_device(int *dev, int *num_sms)
     return W8A8_OK;
 }
 
+// cuTensorMapEncodeTiled (of the device that current_device() found). It wants a context bound to
+// the calling thread, which a host thread without a call of the runtime so far does not have: the
+// threads of PyTorch's backward pass, for one.
+template <typename... Args> CUresult encode_tiled(Args... args)
+{
+    CUresult r = g_encode(args...);
+    int dev = -1;
+    if (r == CUDA_ERROR_INVALID_CONTEXT && cudaGetDevice(&dev) == cudaSuccess &&
+        cudaSetDevice(dev) == cudaSuccess)
+        r = g_encode(args...);
+    return r;
+}
+
 // Once per kernel and device: raise the dynamic shared-memory limit, and ask for the
 // largest shared-memory carveout for every kernel of the library, so consecutive launches
 // of row kernels and GEMMs never reconfigure the L1/shared split between them.
