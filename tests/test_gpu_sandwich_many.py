@@ -112,7 +112,7 @@ KINDS = [("none", False, False), ("none", True, True), ("token", True, False),
 # one, two and four warps a row, with up to sixteen, eight and four rows of an SM at a time, three
 # rows and more each; then one row a CTA with more rows than resident CTAs (narrow rows of few
 # values in all; rows of more than 8192)
-@pytest.mark.parametrize("M,K", [(8003, 208), (2501, 2064), (1301, 4112), (1301, 8192),
+@pytest.mark.parametrize("M,K", [(100003, 16), (33001, 48), (8003, 208), (2501, 2064), (1301, 4112), (1301, 8192),
                                  (20011, 64), (5501, 272), (761, 2064), (601, 14336),
                                  (301, 32768)])
 @pytest.mark.parametrize("kind,post,f8", KINDS)
