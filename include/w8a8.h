@@ -25,7 +25,8 @@
  *   - Base pointers of vectors read or written 16 bytes at a time must be 16-byte aligned
  *     (stated per argument); otherwise W8A8_ERR_ALIGNMENT.
  *   - Inputs must be finite; results for NaN or Inf inputs are unspecified.
- *   - Calls are thread-safe; the only mutable host state is a once-per-process init.
+ *   - Calls are thread-safe, from any host thread (one without a CUDA context gets the current
+ *     device's primary one); the only mutable host state is a once-per-process init.
  *   - There is no CPU fallback: without a B200-class device a call returns
  *     W8A8_ERR_NO_DEVICE.
  */
